@@ -68,10 +68,14 @@ typedef enum {
   MOE_ERR_WORKSPACE = 3,      /* workspace missing, too small or misaligned  */
   MOE_ERR_CUDA = 4,           /* a CUDA runtime call failed                  */
   MOE_ERR_DEVICE_TIMEOUT = 5, /* a bounded device-side wait ran out          */
-  MOE_ERR_DEVICE_RANGE = 6    /* an input outside the exact range of the FP4
+  MOE_ERR_DEVICE_RANGE = 6,   /* an input outside the exact range of the FP4
                                  path (a block scale, or x / h beyond f16);
                                  recorded on the device, the output is not
                                  exact                                       */
+  MOE_ERR_DEVICE_INDEX = 7     /* an index read on the device (a position, a
+                                 cache slot, a page, a length) lies outside
+                                 its table; recorded on the device, the access
+                                 is not made                                 */
 } moe_status;
 
 typedef enum {
@@ -377,9 +381,10 @@ MOE_API moe_status moe_ffn_forward_mx(const moe_bf16* x, int T, int H, int I, co
                                       cudaStream_t stream);
 
 /* Synchronises `stream`, reads the device status word of a workspace used by
- * moe_route() or moe_ffn_forward(), and clears it.  Returns MOE_OK or the
- * first device-side error recorded (MOE_ERR_DEVICE_TIMEOUT, or
- * MOE_ERR_DEVICE_RANGE from the FP4 path); *info_out (if not NULL) receives
+ * any entry point, and clears it.  Returns MOE_OK or the
+ * first device-side error recorded (MOE_ERR_DEVICE_TIMEOUT,
+ * MOE_ERR_DEVICE_RANGE from the FP4 path, or MOE_ERR_DEVICE_INDEX from the
+ * attention side); *info_out (if not NULL) receives
  * the kernel-specific detail word (for MOE_ERR_DEVICE_TIMEOUT: which wait
  * ran out; MOE_INFO_HOLD for the start gate below).
  *
@@ -427,6 +432,63 @@ MOE_API moe_status moe_set_l2_prefetch(const void* const* ptrs, const size_t* by
  * events are recorded as external event-record nodes of the graph, so every
  * replay records them. */
 MOE_API void moe_set_profile_events(void* const* events, int n_pairs);
+
+/* ---- The attention side of the decoder layer around the MoE FFN: what runs
+ * between a layer's input and its FFN in a draft or target model that serves
+ * verify blocks.  The pages keep attention out of the FFN; these entry points
+ * have no counterpart there.  Conventions as above, except that the 16-bit
+ * tensors are bf16 or f16 (`dtype`, one type per call), that rows may be
+ * strided where a stride is named (in elements, a multiple of 8), and that
+ * every index the device reads is checked there: one outside its table is
+ * recorded as MOE_ERR_DEVICE_INDEX in the workspace's status and its access
+ * is not made.  Every workspace is 256-byte aligned and zero-filled once
+ * before its first use; the fixed header that the other entry points keep
+ * counters in is left alone, so one workspace that is large enough serves
+ * calls of all of them, one after another. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_STATUS_BYTES 256 /* the status block at the start of a workspace */
+#define MOE_MAX_ATTN_TOKENS 1048576
+
+/* info words of MOE_ERR_DEVICE_INDEX */
+#define MOE_INFO_POSITION 17 /* a position outside [0, max_pos)               */
+#define MOE_INFO_SLOT 18     /* a cache slot at or past n_slots               */
+
+/* Norms of the query and key heads, the position rotation and the cache
+ * write, in one launch.  For every head row x of D elements, in fp32:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (no norm where weight is NULL)
+ *   then for the i-th of rot_dim/2 pairs (a, b), with c, s the cosine and sine
+ *   of the token's position: (a, b) -> (a c - b s, b c + a s)
+ * rounded once to the output type.
+ *   q, k, v      [T] rows of Hq, Hkv, Hkv heads of D contiguous elements, the
+ *                rows q_stride, k_stride, v_stride elements apart (slices of a
+ *                fused projection's rows, for instance)
+ *   q_weight, k_weight [D] or NULL
+ *   rope         [max_pos, rot_dim] fp32: rot_dim/2 cosines, then as many
+ *                sines; NULL when rot_dim is 0 (no rotation)
+ *   interleaved  0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)
+ *   positions    [T] int32 rows of rope; NULL when rot_dim is 0.  A token
+ *                whose position is outside [0, max_pos) is recorded
+ *                (MOE_INFO_POSITION) and skipped: nothing of it is written
+ *   q_out        rows of Hq x D, q_out_stride elements apart; may be q itself
+ *                with q's stride
+ *   k_cache, v_cache [n_slots, Hkv, D]: a cache of pages is the same rows,
+ *                slot = page * page_size + offset.  v and v_cache may both be
+ *                NULL
+ *   slots        [T] int32: row of the cache that takes the token's keys and
+ *                values (distinct tokens, distinct slots); negative: padding,
+ *                not cached; at or past n_slots: recorded (MOE_INFO_SLOT), not
+ *                cached.  NULL: token t goes to row t (then n_slots >= T)
+ *   ws           >= MOE_STATUS_BYTES bytes
+ * Hq or Hkv may be 0.  Limits: D 64, 128 or 256; rot_dim a multiple of 16,
+ * <= D; T <= MOE_MAX_ATTN_TOKENS; Hq, Hkv <= 1024; pointers 16-byte aligned. */
+MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                                    const void* v, long long v_stride, int T, int Hq, int Hkv, int D, int dtype,
+                                    const void* q_weight, const void* k_weight, float eps, const float* rope,
+                                    int rot_dim, int max_pos, int interleaved, const int32_t* positions,
+                                    void* q_out, long long q_out_stride, void* k_cache, void* v_cache,
+                                    const int32_t* slots, long long n_slots, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -30,19 +30,6 @@ thread_local int t_schedule = MOE_SCHEDULE_AUTO;
 thread_local int t_overlap = 1;  // slice launches overlap the previous kernel on the stream
 thread_local L2Prefetch t_prefetch = {};  // consumed by the next forward on this thread
 
-int device_sms() {
-  int d = 0;
-  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 0;
-  int v = g_sms[d].load(std::memory_order_relaxed);
-  if (v == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) return 0;
-    v = n < kMaxGrid ? n : kMaxGrid;  // one GEMM CTA per SM, up to the span table's size
-    g_sms[d].store(v, std::memory_order_relaxed);
-  }
-  return v;
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -401,6 +388,37 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 namespace moe {
 
+int device_sms() {
+  int d = 0;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 0;
+  int v = g_sms[d].load(std::memory_order_relaxed);
+  if (v == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) return 0;
+    v = n < kMaxGrid ? n : kMaxGrid;  // one GEMM CTA per SM, up to the span table's size
+    g_sms[d].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+bool encode_map_16(CUtensorMap* m, bool f16, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 moe_status route_check_args(const moe_bf16* x, int T, int H, const moe_bf16* gate, const moe_recipe* recipe,
                             const int32_t* topk_idx, const float* topk_w) {
   const moe_status st = check_recipe(recipe);
@@ -426,6 +444,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
     case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT";
     case MOE_ERR_DEVICE_RANGE: return "MOE_ERR_DEVICE_RANGE";
+    case MOE_ERR_DEVICE_INDEX: return "MOE_ERR_DEVICE_INDEX";
   }
   return "MOE_ERR_UNKNOWN";
 }

@@ -17,7 +17,7 @@ namespace moe {
 // ----------------------------------------------------------------------------
 // status word (first 8 bytes of every workspace): {code, info}
 // ----------------------------------------------------------------------------
-enum : int32_t { kStatusTimeout = 5, kStatusRange = 6 };
+enum : int32_t { kStatusTimeout = 5, kStatusRange = 6, kStatusIndex = 7 };
 // info values: which wait ran out
 enum : int32_t {
   kInfoEmpty = 1, kInfoFull = 2, kInfoAccFull = 3, kInfoAccEmpty = 4,
@@ -30,7 +30,11 @@ enum : int32_t {
   kInfoHold = 15,
   // the router's work list is outside the bounds the host computed (a
   // workspace that was not zero-filled before its first use, or overwritten)
-  kInfoWorkList = 16
+  kInfoWorkList = 16,
+  // index errors (kStatusIndex) of the attention operators: a position outside
+  // the rotation table, a cache slot outside the cache, a page outside the
+  // cache, a length outside its page table, block starts out of order
+  kInfoPosition = 17, kInfoSlot = 18, kInfoPage = 19, kInfoLength = 20, kInfoStarts = 21
 };
 
 // ----------------------------------------------------------------------------
@@ -368,6 +372,15 @@ constexpr int kStatusHoldWord = 2;
 moe_status route_check_args(const uint16_t* x, int T, int H, const uint16_t* gate, const moe_recipe* recipe,
                             const int32_t* topk_idx, const float* topk_w);
 
+// Host helpers of api.cu shared with the other entry points' files: the SM
+// count of the current device (0 on failure); a tensor map over a 16-bit
+// tensor (bf16, or f16), dims and box from the contiguous dimension outwards
+// and the strides of all but it in bytes, with the 128-byte swizzle and zeros
+// out of range.
+int device_sms();
+bool encode_map_16(CUtensorMap* m, bool f16, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box);
+
 // launchers (route.cu, gemm.cu, combine.cu); return cudaError_t
 cudaError_t launch_route(const RouteParams& p, int tb, cudaStream_t s);
 // Tiled CUDA-core logits GEMM for many tokens (the router's first step).
@@ -643,6 +656,11 @@ __device__ __forceinline__ void record_failure(int32_t* status, volatile int* ab
 // runs on (its output is not exact).
 __device__ __forceinline__ void record_range(int32_t* status, int32_t info) {
   if (atomicCAS(status, 0, kStatusRange) == 0) atomicExch(status + 1, info);
+}
+
+// An index outside its table: recorded, the access is not made.
+__device__ __forceinline__ void record_index(int32_t* status, int32_t info) {
+  if (atomicCAS(status, 0, kStatusIndex) == 0) atomicExch(status + 1, info);
 }
 
 __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {

@@ -18,11 +18,16 @@ LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT,
- MOE_ERR_DEVICE_RANGE) = range(7)
+ MOE_ERR_DEVICE_RANGE, MOE_ERR_DEVICE_INDEX) = range(8)
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRTSOFTPLUS = 0, 1, 2
 # the workspace's start gate (include/moe.h) and the info word of its timeout
 WS_HOLD_OFFSET = 8
 INFO_HOLD = 15
+# the status block at a workspace's start, and the info words of an index
+# outside its table (include/moe.h)
+STATUS_BYTES = 256
+INFO_POSITION, INFO_SLOT = 17, 18
+DTYPE_BF16, DTYPE_F16 = 0, 1
 # routed-expert formats of the block-scaled path
 FMT_FP4, FMT_FP8 = 1, 2
 
@@ -67,6 +72,8 @@ _lib_handle: Optional[ctypes.CDLL] = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_route_workspace_bytes": (_SZ, [_I, _I]),
@@ -92,6 +99,8 @@ _SIGS = {
     "moe_mx_prepare_scales": (_I, [_I, _P, _P, _I, _I, _I, _P, _P, _I, _P, _SZ, _P]),
     "moe_ffn_forward_mx": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _SZ,
                                 ctypes.POINTER(Recipe), _P, _SZ, _P, _P, _P, _P, _P]),
+    "moe_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _I, _I, _P, _P, _L,
+                              _P, _P, _P, _L, _P, _SZ, _P]),
 }
 
 SCHEDULE_AUTO, SCHEDULE_STREAM_K, SCHEDULE_SLICE = 0, 1, 2
@@ -374,6 +383,117 @@ def moe_ffn_forward_mx(x, gate, routed_fmt: int, w_gate_up_q, w_down_q, scales, 
         _ptr(_u8(scales)), scales.numel(), ctypes.byref(recipe), ws.ptr(), ws.nbytes, _ptr(y), _ptr(topk_idx_out),
         _ptr(topk_w_out), _ptr(counts_out), _stream(stream)), "moe_ffn_forward_mx")
     return y
+
+
+# --------------------------------------------------------------------------- the attention side of the layer
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _dtype16(t: torch.Tensor, *others) -> int:
+    """The library's code of a call's one 16-bit type."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("expected a bfloat16 or float16 tensor")
+    for o in others:
+        if o is not None and o.dtype != t.dtype:
+            raise TypeError("the 16-bit tensors of a call have one type")
+    return code
+
+
+def _typed(t: Optional[torch.Tensor], dtype, name: str) -> None:
+    if t is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected a {dtype} tensor")
+
+
+def _heads(t: torch.Tensor, name: str):
+    """(heads, D, row stride) of a [T, heads, D] tensor on the GPU whose rows
+    may lie apart (a slice of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError("tensor is not on a CUDA device")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [T, heads, D]")
+    h, d = t.shape[1], t.shape[2]
+    s = t.stride()
+    if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        raise ValueError(f"{name}: the heads of a row are not contiguous")
+    return h, d, (s[0] if t.shape[0] > 1 else h * d)
+
+
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, scale: float = 1.0,
+               device=None) -> torch.Tensor:
+    """Cosines and sines of every position for ``qk_norm_rope``: fp32
+    [max_positions, rot_dim], the angles position * scale * base^(-2i/rot_dim)
+    taken in 64 bits.  Any other table of that layout serves as well."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, device=device, dtype=torch.float64) / rot_dim)
+    angle = torch.arange(max_positions, device=device, dtype=torch.float64)[:, None] * (scale * inv)
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float()
+
+
+def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_cache=None, v_cache=None, slots=None, stream=None):
+    """RMS norms of the query and key heads, the position rotation and the
+    cache write in one launch (moe_qk_norm_rope).
+
+    q [T,Hq,D], k, v [T,Hkv,D] (rows may lie apart, e.g. slices of a fused
+    projection); positions int32 [T], rope fp32 [max_pos, rot_dim]
+    (``rope_table``), both None for no rotation; q_weight, k_weight [D] or None
+    for no norm; k_cache, v_cache contiguous [..., Hkv, D]
+    ([pages, page_size, Hkv, D] for a cache of pages), slots int32 [T] their
+    rows (negative: not cached; None: row t).  q, k and v may be None.
+    -> (q_out, k_cache, v_cache); buffers that are not given are made."""
+    first = q if q is not None else k
+    T = first.shape[0]
+    Hq = Hkv = qs = ks = vs = qos = 0
+    D = first.shape[2]
+    dt = _dtype16(first, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache)
+    _need_cuda(positions, rope, q_weight, k_weight, slots, k_cache, v_cache)
+    _typed(positions, torch.int32, "positions")
+    _typed(slots, torch.int32, "slots")
+    _typed(rope, torch.float32, "rope")
+    if q is not None:
+        Hq, _, qs = _heads(q, "q")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        qos = _heads(q_out, "q_out")[2]
+        if q_out.shape != q.shape:
+            raise ValueError("q_out: expected the shape of q")
+    if k is not None:
+        Hkv, dk, ks = _heads(k, "k")
+        if k.shape[0] != T or dk != D:
+            raise ValueError("k: expected the tokens and head size of q")
+        if k_cache is None:
+            if slots is not None:
+                raise ValueError("slots name rows of a cache: pass k_cache")
+            k_cache = torch.empty((T, Hkv, D), dtype=k.dtype, device=k.device)
+    n_slots = 0
+    if v is not None:
+        if k is None or v.shape != k.shape:
+            raise ValueError("v: expected the shape of k")
+        vs = _heads(v, "v")[2]
+        if v_cache is None:
+            if slots is not None:
+                raise ValueError("slots name rows of a cache: pass v_cache")
+            v_cache = torch.empty((T, Hkv, D), dtype=v.dtype, device=v.device)
+    elif v_cache is not None:
+        raise ValueError("v_cache without v")
+    for c in (k_cache, v_cache):
+        if c is not None and (Hkv == 0 or c.dim() < 2 or c.shape[-1] != D or c.shape[-2] != Hkv or
+                              c.numel() != k_cache.numel()):
+            raise ValueError("caches: expected [..., Hkv, D] of one size")
+    if k_cache is not None:
+        n_slots = k_cache.numel() // (Hkv * D)
+    rot, max_pos = (0, 0) if rope is None else (rope.shape[1], rope.shape[0])
+    for t, n, name in ((positions, T, "positions"), (slots, T, "slots"), (q_weight, D, "q_weight"),
+                       (k_weight, D, "k_weight")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name}: expected {n} elements")
+    _check(lib().moe_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, Hq, Hkv, D, dt, _ptr(q_weight),
+                                  _ptr(k_weight), eps, _ptr(rope), rot, max_pos, 1 if interleaved else 0,
+                                  _ptr(positions), _ptr(q_out), qos, _ptr(k_cache), _ptr(v_cache), _ptr(slots),
+                                  n_slots, ws.ptr(), ws.nbytes, _stream(stream)), "moe_qk_norm_rope")
+    return q_out, k_cache, v_cache
 
 
 def set_schedule(schedule: int) -> None:
