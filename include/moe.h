@@ -453,6 +453,9 @@ MOE_API void moe_set_profile_events(void* const* events, int n_pairs);
 /* info words of MOE_ERR_DEVICE_INDEX */
 #define MOE_INFO_POSITION 17 /* a position outside [0, max_pos)               */
 #define MOE_INFO_SLOT 18     /* a cache slot at or past n_slots               */
+#define MOE_INFO_PAGE 19     /* a page outside [0, n_pages)                   */
+#define MOE_INFO_LENGTH 20   /* a length below 0 or past its page table       */
+#define MOE_INFO_STARTS 21   /* block starts out of order or outside [0, T]   */
 
 /* Norms of the query and key heads, the position rotation and the cache
  * write, in one launch.  For every head row x of D elements, in fp32:
@@ -489,6 +492,53 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
                                     void* q_out, long long q_out_stride, void* k_cache, void* v_cache,
                                     const int32_t* slots, long long n_slots, void* ws, size_t ws_bytes,
                                     cudaStream_t stream);
+
+/* Attention of a batch of B requests over a cache of pages.  Every request's
+ * context is one prefix that all of them share (a system prompt, a document),
+ * read once for the whole batch, followed by keys of its own; its queries are
+ * the n tokens of its block (one token of decoding, a verify block, a draft
+ * block, a prompt), whose own keys are in the cache already (moe_qk_norm_rope
+ * writes them).  For the i-th token of a request and every head, over the
+ * prefix keys and the first `seen` of the request's own keys
+ *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ *   seen = own_len where causal is 0 (every token of a draft block sees the
+ *   whole block), else max(0, own_len - n + i + 1)
+ * in fp32 (the probabilities enter the second product in the 16-bit type),
+ * rounded once.  A token that sees no key, or that belongs to no request, gets
+ * out = 0 and lse = -infinity.
+ *   q            [T] rows of Hq x D, q_stride elements apart
+ *   q_start      [B+1] int32: request b has the tokens [q_start[b],
+ *                q_start[b+1]), in order; tokens outside (padding) are allowed
+ *   k_cache, v_cache [n_pages, page_size, Hkv, D]; query head h reads key head
+ *                h / (Hq / Hkv).  Slots that no length covers may hold
+ *                anything; covered ones hold finite values
+ *   prefix_pages [prefix_cap] int32, prefix_len [1] int32: key j < prefix_len is
+ *                slot j % page_size of page prefix_pages[j / page_size];
+ *                prefix_cap 0: no prefix (then both may be NULL)
+ *   page_table   [B, table_width] int32, own_len [B] int32: each request's own
+ *                keys, likewise; table_width 0: none (then both may be NULL)
+ *   out          [T, Hq, D], not q
+ *   lse          [T, Hq] fp32 or NULL (natural logarithm)
+ *   ws           >= moe_prefix_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes
+ * All lengths and tables stay on the device, so a captured call serves later
+ * steps of the same T and B.  A page outside [0, n_pages) is recorded
+ * (MOE_INFO_PAGE) and read as zeros; a length outside its table is recorded
+ * (MOE_INFO_LENGTH) and held within it; a request whose starts are out of
+ * order or outside [0, T] is recorded (MOE_INFO_STARTS) and its tokens' output
+ * is not defined.
+ * Limits: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 128, Hq <= 1024;
+ * page_size a power of two from 8 to 1024; T <= MOE_MAX_ATTN_TOKENS, B <=
+ * MOE_MAX_REQUESTS, prefix_cap and table_width times page_size <=
+ * MOE_MAX_KEYS; 0 < scale < infinity; pointers 16-byte aligned. */
+#define MOE_MAX_REQUESTS 65536
+#define MOE_MAX_KEYS 268435456
+MOE_API size_t moe_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+MOE_API moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B, const int32_t* q_start,
+                                        int Hq, int Hkv, int D, int dtype, const void* k_cache, const void* v_cache,
+                                        int n_pages, int page_size, const int32_t* prefix_pages, int prefix_cap,
+                                        const int32_t* prefix_len, const int32_t* page_table, int table_width,
+                                        const int32_t* own_len, int causal, float scale, void* out, float* lse,
+                                        void* ws, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

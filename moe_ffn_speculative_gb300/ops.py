@@ -26,7 +26,7 @@ INFO_HOLD = 15
 # the status block at a workspace's start, and the info words of an index
 # outside its table (include/moe.h)
 STATUS_BYTES = 256
-INFO_POSITION, INFO_SLOT = 17, 18
+INFO_POSITION, INFO_SLOT, INFO_PAGE, INFO_LENGTH, INFO_STARTS = 17, 18, 19, 20, 21
 DTYPE_BF16, DTYPE_F16 = 0, 1
 # routed-expert formats of the block-scaled path
 FMT_FP4, FMT_FP8 = 1, 2
@@ -101,6 +101,9 @@ _SIGS = {
                                 ctypes.POINTER(Recipe), _P, _SZ, _P, _P, _P, _P, _P]),
     "moe_qk_norm_rope": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _I, _I, _P, _P, _L,
                               _P, _P, _P, _L, _P, _SZ, _P]),
+    "moe_prefix_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_prefix_attention": (_I, [_P, _L, _I, _I, _P, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I, _P, _I, _F,
+                                  _P, _P, _P, _SZ, _P]),
 }
 
 SCHEDULE_AUTO, SCHEDULE_STREAM_K, SCHEDULE_SLICE = 0, 1, 2
@@ -494,6 +497,57 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
                                   _ptr(positions), _ptr(q_out), qos, _ptr(k_cache), _ptr(v_cache), _ptr(slots),
                                   n_slots, ws.ptr(), ws.nbytes, _stream(stream)), "moe_qk_norm_rope")
     return q_out, k_cache, v_cache
+
+
+def prefix_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    n = lib().moe_prefix_attention_workspace_bytes(T, B, Hq, Hkv, D)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_prefix_attention_workspace_bytes")
+    return n
+
+
+def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, page_table, own_len, ws: Workspace,
+                     causal: bool = True, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention of a batch of requests over a prefix that all of them share
+    and pages of their own (moe_prefix_attention).
+
+    q [T,Hq,D] (rows may lie apart); k_cache, v_cache [pages, page_size, Hkv, D];
+    q_start int32 [B+1]; prefix_pages int32 [n] with prefix_len int32 [1], or
+    both None; page_table int32 [B, width] with own_len int32 [B], or both
+    None; scale 1/sqrt(D) unless given; lse fp32 [T,Hq] is written when given.
+    -> out [T,Hq,D]."""
+    dt = _dtype16(q, k_cache, v_cache, out)
+    _need_cuda(k_cache, v_cache, q_start, prefix_pages, prefix_len, page_table, own_len, out, lse)
+    Hq, D, qs = _heads(q, "q")
+    T, B = q.shape[0], q_start.numel() - 1
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != D:
+        raise ValueError("caches: expected [pages, page_size, Hkv, D] of one shape")
+    if B < 0 or (prefix_pages is None) != (prefix_len is None) or (page_table is None) != (own_len is None):
+        raise ValueError("q_start has B+1 elements; page lists come with their lengths")
+    pages, page, Hkv, _ = k_cache.shape
+    for t, name in ((q_start, "q_start"), (prefix_pages, "prefix_pages"), (prefix_len, "prefix_len"),
+                    (page_table, "page_table"), (own_len, "own_len")):
+        _typed(t, torch.int32, name)
+    _typed(lse, torch.float32, "lse")
+    cap = width = 0
+    if prefix_pages is not None:
+        cap = prefix_pages.numel()
+        if prefix_len.numel() != 1:
+            raise ValueError("prefix_len: expected one element")
+    if page_table is not None:
+        if page_table.dim() != 2 or page_table.shape[0] != B or own_len.numel() != B:
+            raise ValueError("page_table: expected [B, width], own_len: [B]")
+        width = page_table.shape[1]
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
+        raise ValueError("out: expected the shape of q, lse: [T, Hq]")
+    _check(lib().moe_prefix_attention(_ptr(q), qs, T, B, _ptr(q_start), Hq, Hkv, D, dt, _ptr(k_cache), _ptr(v_cache),
+                                      pages, page, _ptr(prefix_pages), cap, _ptr(prefix_len), _ptr(page_table), width,
+                                      _ptr(own_len), 1 if causal else 0, D ** -0.5 if scale is None else scale,
+                                      _ptr(out), _ptr(lse), ws.ptr(), ws.nbytes, _stream(stream)),
+           "moe_prefix_attention")
+    return out
 
 
 def set_schedule(schedule: int) -> None:
