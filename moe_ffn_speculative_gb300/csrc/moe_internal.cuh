@@ -34,7 +34,11 @@ enum : int32_t {
   // index errors (kStatusIndex) of the attention operators: a position outside
   // the rotation table, a cache slot outside the cache, a page outside the
   // cache, a length outside its page table, block starts out of order
-  kInfoPosition = 17, kInfoSlot = 18, kInfoPage = 19, kInfoLength = 20, kInfoStarts = 21
+  kInfoPosition = 17, kInfoSlot = 18, kInfoPage = 19, kInfoLength = 20, kInfoStarts = 21,
+  // waits of the shared-prefix attention: a key/value stage, a query tile, the
+  // scores, the probabilities, the output tile, copies or MMAs in flight
+  kInfoAttnStage = 22, kInfoAttnQuery = 23, kInfoAttnScores = 24, kInfoAttnProbs = 25, kInfoAttnOut = 26,
+  kInfoAttnDrain = 27
 };
 
 // ----------------------------------------------------------------------------
