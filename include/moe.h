@@ -540,6 +540,32 @@ MOE_API moe_status moe_prefix_attention(const void* q, long long q_stride, int T
                                         const int32_t* own_len, int causal, float scale, void* out, float* lse,
                                         void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* Matrix product with its epilogue (the projections before and after the
+ * attention, a dense MLP's layers): for every row x_m of K elements
+ *   y_m = act(x_m W^T + bias) + residual_m
+ * with fp32 accumulation of the exact products, the epilogue in fp32 and one
+ * rounding.
+ *   x          [M] rows of K, x_stride elements apart
+ *   w          [N, K]         bias [N] or NULL
+ *   activation MOE_ACT_*      gelu is 0.5 v (1 + erf(v / sqrt 2)), gelu_tanh
+ *              0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))), silu v / (1 + e^-v)
+ *   residual   [M] rows of N, residual_stride elements apart, or NULL; may be
+ *              y itself with y's stride
+ *   y          [M] rows of N, y_stride elements apart; overlaps neither x nor w
+ *   ws         >= moe_linear_workspace_bytes(M, N, K) bytes
+ * Limits: N and K multiples of 8; M, N, K <= MOE_MAX_LINEAR; pointers 16-byte
+ * aligned. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1
+#define MOE_ACT_GELU 2
+#define MOE_ACT_GELU_TANH 3
+#define MOE_ACT_RELU 4
+#define MOE_MAX_LINEAR 1048576
+MOE_API size_t moe_linear_workspace_bytes(int M, int N, int K);
+MOE_API moe_status moe_linear(const void* x, long long x_stride, int M, int K, const void* w, int N, int dtype,
+                              const void* bias, int activation, const void* residual, long long residual_stride,
+                              void* y, long long y_stride, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

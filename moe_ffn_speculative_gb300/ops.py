@@ -104,6 +104,8 @@ _SIGS = {
     "moe_prefix_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_prefix_attention": (_I, [_P, _L, _I, _I, _P, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _I, _P, _I, _F,
                                   _P, _P, _P, _SZ, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_linear": (_I, [_P, _L, _I, _I, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _SZ, _P]),
 }
 
 SCHEDULE_AUTO, SCHEDULE_STREAM_K, SCHEDULE_SLICE = 0, 1, 2
@@ -548,6 +550,56 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
                                       _ptr(out), _ptr(lse), ws.ptr(), ws.nbytes, _stream(stream)),
            "moe_prefix_attention")
     return out
+
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+
+def linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = lib().moe_linear_workspace_bytes(M, N, K)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_linear_workspace_bytes")
+    return n
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of a matrix on the GPU whose rows may lie apart."""
+    if not t.is_cuda:
+        raise ValueError("tensor is not on a CUDA device")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    s, n = t.stride(), t.shape[1]
+    if n > 1 and s[1] != 1:
+        raise ValueError(f"{name}: the elements of a row are not contiguous")
+    return s[0] if t.shape[0] > 1 else n
+
+
+def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=None, y=None, stream=None):
+    """act(x w^T + bias) + residual (moe_linear): x [M,K], w [N,K], bias [N],
+    residual [M,N]; activation one of ACTIVATIONS; rows of x, residual and y
+    may lie apart; residual may be y.  -> y [M,N]."""
+    dt = _dtype16(x, w, bias, residual, y)
+    _need_cuda(w, bias)
+    xs = _rows(x, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    if w.dim() != 2 or w.shape[1] != K or (bias is not None and bias.numel() != N):
+        raise ValueError("w: expected [N, K], bias: [N]")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unknown activation {activation!r}")
+    if y is None:
+        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    ys, rs = _rows(y, "y"), 0
+    if residual is not None:
+        rs = _rows(residual, "residual")
+        if residual.shape != y.shape:
+            raise ValueError("residual: expected [M, N]")
+    if y.shape != (M, N):
+        raise ValueError("y: expected [M, N]")
+    _check(lib().moe_linear(_ptr(x), xs, M, K, _ptr(w), N, dt, _ptr(bias), act, _ptr(residual), rs, _ptr(y), ys,
+                            ws.ptr(), ws.nbytes, _stream(stream)), "moe_linear")
+    return y
 
 
 def set_schedule(schedule: int) -> None:
