@@ -11,6 +11,14 @@
 //
 // A CTA: warp 0 loads weight and token tiles by TMA into a ring of stages,
 // warp 1 issues the MMAs, warps 2..5 drain tensor memory.
+//
+// Many rows: bound by the tensor cores.  Pairs of CTAs work on tiles of 256
+// tokens by up to 256 outputs (linear_many_kernel): each CTA holds 128 token
+// rows and half of the tile's weight rows, and the pair's MMA reads both
+// halves, so a byte of shared memory feeds twice the products.  The pairs are
+// persistent; two accumulators in tensor memory let a tile's epilogue run
+// under the next tile's products.  The tile's width is chosen so that the last
+// wave of tiles is full.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -25,12 +33,12 @@ namespace {
 constexpr int kLinThreads = 192;
 constexpr int kLinSmem = 232448 - 1024;  // 227 KB less the control words
 constexpr int kLinMaxStages = 12;
-constexpr int kLinMaxTokens = 256;       // tokens of a tile
+constexpr int kFewTokens = 128;          // up to this many rows: linear_few_kernel, one tile of tokens
 constexpr int kMaxCluster = 8;
 
 struct LinearParams {
   int M, N, K, k_blocks;
-  int n_tok;                 // tokens of a tile: a multiple of 16
+  int n_tok;                 // few rows: tokens of a tile; many: its outputs (a multiple of 16)
   int stages, cluster;
   uint32_t tmem_cols;
   const uint16_t *bias, *residual;
@@ -99,7 +107,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = p.cluster > 1 ? cluster_rank() : 0;
   const int n0 = (blockIdx.x / p.cluster) * kHalfRows;
-  const int t0 = blockIdx.y * p.n_tok;
   const int kb0 = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / p.cluster);
   const int kb1 = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / p.cluster);
   const uint32_t stage_bytes = kTileBytesA + p.n_tok * 128;
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint8_t* a = ring_mem + r.stage * stage_bytes;
         mbar_arrive_expect_tx(&c.full[r.stage], stage_bytes);
         tma_load_2d_hint(a, &tm_w, &c.full[r.stage], kb * kBlockK, n0, pol);
-        tma_load_2d(a + kTileBytesA, &tm_x, &c.full[r.stage], kb * kBlockK, t0);
+        tma_load_2d(a + kTileBytesA, &tm_x, &c.full[r.stage], kb * kBlockK, 0);
         ++filled;
         r.next(p.stages);
       }
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   // the tile's rows are lanes; warp w of 2..5 reads lanes 32 (w % 4) ..
   const int row = (warp & 3) * 32 + lane;
-  const int toks = min(p.n_tok, p.M - t0);
+  const int toks = p.M;
   if (p.cluster == 1) {
     if (warp >= 2 && ok) {
       const int n = n0 + row;
@@ -189,8 +196,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (n < p.N)
           for (int i = 0; i < 16 && t + i < toks; ++i) {
             float v = activate(__uint_as_float(r[i]) + bias, p.act);
-            if (p.residual) v += to_f<kBf16>(p.residual[(t0 + t + i) * p.res_stride + n]);
-            p.y[(t0 + t + i) * p.y_stride + n] = from_f<kBf16>(v);
+            if (p.residual) v += to_f<kBf16>(p.residual[(t + i) * p.res_stride + n]);
+            p.y[(t + i) * p.y_stride + n] = from_f<kBf16>(v);
           }
       }
     }
@@ -224,10 +231,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint16_t* o = &out.x;
         for (int i = 0; i < 4; ++i) {
           float z = activate(v[i] + bias[i], p.act);
-          if (p.residual) z += to_f<kBf16>(p.residual[(t0 + t) * p.res_stride + n + i]);
+          if (p.residual) z += to_f<kBf16>(p.residual[t * p.res_stride + n + i]);
           o[i] = from_f<kBf16>(z);
         }
-        *reinterpret_cast<ushort4*>(p.y + (t0 + t) * p.y_stride + n) = out;
+        *reinterpret_cast<ushort4*>(p.y + t * p.y_stride + n) = out;
       }
     }
     cluster_sync();  // the others have read this CTA's sums
@@ -237,6 +244,277 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------- many rows: CTA pairs
+constexpr int kManyThreads = 320;  // producer, issuer, 8 epilogue warps
+constexpr int kManyEpiWarps = 8;
+constexpr int kManyStages = 6;
+constexpr int kManyRows = 256;     // tokens of a tile, 128 a CTA
+constexpr int kManyWide = 256;     // widest tile, in outputs
+
+struct ManyControl {
+  uint64_t full[kManyStages], empty[kManyStages], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__device__ __forceinline__ uint32_t map_rank(const void* local, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  return a;
+}
+// TMA load into this CTA's shared memory, counted on a barrier of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at the same place in both CTAs of the pair when the
+// MMAs issued so far are complete.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = to_f<kBf16>(static_cast<uint16_t>(w[i] & 0xffffu));
+    f[2 * i + 1] = to_f<kBf16>(static_cast<uint16_t>(w[i] >> 16));
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = static_cast<uint32_t>(from_f<kBf16>(f[2 * i])) | (static_cast<uint32_t>(from_f<kBf16>(f[2 * i + 1])) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One row's 16 outputs from column n (a multiple of 8 of them below N).
+template <bool kBf16, int kAct>
+__device__ __forceinline__ void finish16(const LinearParams& p, const uint32_t (&r)[16], int t, int n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (n + 8 * h >= p.N) break;
+    float v[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * h + i]);
+    if (p.bias) {
+      unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(p.bias + n + 8 * h)), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kAct);
+    if (p.residual) {
+      unpack8<kBf16>(*reinterpret_cast<const uint4*>(p.residual + t * p.res_stride + n + 8 * h), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    *reinterpret_cast<uint4*>(p.y + t * p.y_stride + n + 8 * h) = pack8<kBf16>(v);
+  }
+}
+
+template <bool kBf16, int kAct>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    linear_many_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                       const __grid_constant__ LinearParams p) {
+  extern __shared__ uint8_t dynamic[];
+  __shared__ ManyControl c;
+  uint8_t* ring_mem = dynamic + ((1024u - (smem_u32(dynamic) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int wide = p.n_tok;  // outputs of a tile
+  const int t_tiles = ceil_div(p.M, kManyRows), tiles = t_tiles * ceil_div(p.N, wide);
+  const uint32_t stage_bytes = kTileBytesA + static_cast<uint32_t>(wide / 2) * 128;
+  const uint32_t stage_space = kTileBytesA + kManyWide / 2 * 128;
+
+  if (tid == 0) {
+    c.abort_flag = 0;
+    for (int s = 0; s < kManyStages; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&c.acc_full[b], 1); mbar_init(&c.acc_empty[b], 2 * kManyEpiWarps); }
+    mbar_init(&c.drain, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    // this CTA's 128 token rows and its half of the tile's weight rows
+    if (lane == 0) {
+      Ring r;
+      int filled = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        const int t0 = (tile % t_tiles) * kManyRows + static_cast<int>(rank) * 128;
+        const int n0 = (tile / t_tiles) * wide + static_cast<int>(rank) * (wide / 2);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          ok = mbar_wait(&c.empty[r.stage], r.phase ^ 1u, &c.abort_flag);
+          if (!ok) break;
+          uint8_t* a = ring_mem + r.stage * stage_space;
+          if (rank == 0) mbar_arrive_expect_tx(&c.full[r.stage], 2 * stage_bytes);
+          const uint32_t bar = map_rank(&c.full[r.stage], 0);
+          tma_load_2d_pair(a, &tm_x, bar, kb * kBlockK, t0);
+          tma_load_2d_pair(a + kTileBytesA, &tm_w, bar, kb * kBlockK, n0);
+          ++filled;
+          r.next(kManyStages);
+        }
+      }
+      if (!ok) record_failure(p.status, &c.abort_flag, kInfoEmpty);
+      // both CTAs' copies are counted on the leader's barriers
+      if (rank == 0)
+        for (int s = 0; s < kManyStages; ++s) {
+          const int fills = filled / kManyStages + (s < filled % kManyStages ? 1 : 0);
+          if (fills > 0 && !mbar_wait(&c.full[s], (fills - 1) & 1, nullptr))
+            record_failure(p.status, &c.abort_flag, kInfoDrain);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t id = kBf16 ? idesc_bf16(kManyRows, wide) : idesc_f16(kManyRows, wide);
+      Ring r;
+      bool ok = true;
+      int i = 0;
+      for (int tile = pair; tile < tiles && ok; tile += pairs, ++i) {
+        const int buf = i & 1;
+        ok = mbar_wait(&c.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &c.abort_flag);
+        if (!ok) { record_failure(p.status, &c.abort_flag, kInfoAccEmpty); break; }
+        tc_fence_after();
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          ok = mbar_wait(&c.full[r.stage], r.phase, &c.abort_flag);
+          if (!ok) { record_failure(p.status, &c.abort_flag, kInfoFull); break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring_mem + r.stage * stage_space), b = a + kTileBytesA;
+#pragma unroll
+          for (int ks = 0; ks < kBlockK / 16; ++ks)
+            mma_pair(tmem + buf * kManyWide, sw128_desc(a + ks * 32), sw128_desc(b + ks * 32), id,
+                     (kb > 0 || ks > 0) ? 1u : 0u);
+          commit_pair(&c.empty[r.stage]);
+          r.next(kManyStages);
+        }
+        commit_pair(&c.acc_full[buf]);
+      }
+      commit_pair(&c.drain);
+      if (!mbar_wait(&c.drain, 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoDrain);
+    }
+  } else {
+    // rows are lanes; two warps a 32-lane quarter, a half of the columns each
+    const int quarter = warp & 3, half = (warp - 2) / 4;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int split = ((wide / 2 + 15) / 16) * 16;
+    int i = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++i) {
+      const int buf = i & 1;
+      const bool got = mbar_wait(&c.acc_full[buf], (i >> 1) & 1, &c.abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) record_failure(p.status, &c.abort_flag, kInfoAccFull);
+        break;
+      }
+      tc_fence_after();
+      const int t = (tile % t_tiles) * kManyRows + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      const int n0 = (tile / t_tiles) * wide;
+      for (int col = half ? split : 0; col < (half ? wide : split); col += 16) {
+        if (n0 + col >= p.N) break;
+        uint32_t r[16];
+        tmem_ld16(tmem + buf * kManyWide + col + lanes, r);
+        tmem_ld_wait();
+        if (t < p.M) finish16<kBf16, kAct>(p, r, t, n0 + col);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(map_rank(&c.acc_empty[buf], 0));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA's copies, MMAs or barriers are in use
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Outputs of a tile: the width that makes the waves of tiles cheapest, a wave
+// costing its width and about 24 outputs' worth of fixed time.
+int tile_width(int M, int N, int pairs) {
+  int best = kManyWide;
+  long long cost = -1;
+  for (int w = kManyWide; w >= 64; w -= 16) {
+    const long long tiles = static_cast<long long>(ceil_div(M, kManyRows)) * ceil_div(N, w);
+    const long long c = (tiles + pairs - 1) / pairs * (w + 24);
+    if (cost < 0 || c < cost) { cost = c; best = w; }
+  }
+  return best;
+}
+
+template <bool kBf16, int kAct>
+cudaError_t launch_many_act(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, int grid,
+                            cudaStream_t s) {
+  const int smem = 1024 + kManyStages * (kTileBytesA + kManyWide / 2 * 128);
+  cudaError_t e =
+      cudaFuncSetAttribute(linear_many_kernel<kBf16, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kManyThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_many_kernel<kBf16, kAct>, tm_w, tm_x, p);
+}
+template <bool kBf16>
+cudaError_t launch_many(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, int grid,
+                        cudaStream_t s) {
+  switch (p.act) {
+    case MOE_ACT_SILU: return launch_many_act<kBf16, MOE_ACT_SILU>(tm_w, tm_x, p, grid, s);
+    case MOE_ACT_GELU: return launch_many_act<kBf16, MOE_ACT_GELU>(tm_w, tm_x, p, grid, s);
+    case MOE_ACT_GELU_TANH: return launch_many_act<kBf16, MOE_ACT_GELU_TANH>(tm_w, tm_x, p, grid, s);
+    case MOE_ACT_RELU: return launch_many_act<kBf16, MOE_ACT_RELU>(tm_w, tm_x, p, grid, s);
+    default: return launch_many_act<kBf16, MOE_ACT_NONE>(tm_w, tm_x, p, grid, s);
   }
 }
 
@@ -257,7 +535,7 @@ cudaError_t launch_few(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const L
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(ceil_div(p.N, kHalfRows) * p.cluster, ceil_div(p.M, p.n_tok));
+  cfg.gridDim = dim3(ceil_div(p.N, kHalfRows) * p.cluster);
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = kLinSmem;
   cfg.stream = s;
@@ -307,13 +585,17 @@ moe_status moe_linear(const void* x, long long x_stride, int M, int K, const voi
   memset(&p, 0, sizeof(p));
   p.M = M; p.N = N; p.K = K;
   p.k_blocks = ceil_div(K, kBlockK);
-  const int m_tiles = ceil_div(M, kLinMaxTokens);
-  p.n_tok = ceil_div(ceil_div(M, m_tiles), 16) * 16;
-  p.cluster = cluster_size(ceil_div(N, kHalfRows) * ceil_div(M, p.n_tok), p.k_blocks, sms);
-  p.stages = (kLinSmem - 1024) / (kTileBytesA + p.n_tok * 128);
-  if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < static_cast<uint32_t>(p.n_tok)) p.tmem_cols <<= 1;
+  const bool few = M <= kFewTokens;
+  if (few) {
+    p.n_tok = ceil_div(M, 16) * 16;
+    p.cluster = cluster_size(ceil_div(N, kHalfRows), p.k_blocks, sms);
+    p.stages = (kLinSmem - 1024) / (kTileBytesA + p.n_tok * 128);
+    if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < static_cast<uint32_t>(p.n_tok)) p.tmem_cols <<= 1;
+  } else {
+    p.n_tok = tile_width(M, N, sms / 2);
+  }
   p.bias = static_cast<const uint16_t*>(bias);
   p.residual = static_cast<const uint16_t*>(residual); p.res_stride = residual_stride;
   p.y = static_cast<uint16_t*>(y); p.y_stride = y_stride;
@@ -324,10 +606,18 @@ moe_status moe_linear(const void* x, long long x_stride, int M, int K, const voi
   const uint64_t wd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N)}, wst[1] = {static_cast<uint64_t>(K) * 2};
   const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
   const uint64_t xst[1] = {static_cast<uint64_t>(M > 1 ? x_stride : K) * 2};
-  const uint32_t wb[2] = {kBlockK, kHalfRows}, xb[2] = {kBlockK, static_cast<uint32_t>(p.n_tok)};
+  const uint32_t wb[2] = {kBlockK, static_cast<uint32_t>(few ? kHalfRows : p.n_tok / 2)};
+  const uint32_t xb[2] = {kBlockK, static_cast<uint32_t>(few ? p.n_tok : kManyRows / 2)};
   if (!encode_map_16(&tm_w, f16, w, 2, wd, wst, wb) || !encode_map_16(&tm_x, f16, x, 2, xd, xst, xb))
     return MOE_ERR_CUDA;
-  const cudaError_t e = f16 ? launch_few<false>(tm_w, tm_x, p, stream) : launch_few<true>(tm_w, tm_x, p, stream);
+  cudaError_t e;
+  if (few) {
+    e = f16 ? launch_few<false>(tm_w, tm_x, p, stream) : launch_few<true>(tm_w, tm_x, p, stream);
+  } else {
+    const long long tiles = static_cast<long long>(ceil_div(M, kManyRows)) * ceil_div(N, p.n_tok);
+    const int grid = 2 * static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    e = f16 ? launch_many<false>(tm_w, tm_x, p, grid, stream) : launch_many<true>(tm_w, tm_x, p, grid, stream);
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
