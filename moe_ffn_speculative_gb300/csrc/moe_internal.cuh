@@ -36,9 +36,10 @@ enum : int32_t {
   // cache, a length outside its page table, block starts out of order
   kInfoPosition = 17, kInfoSlot = 18, kInfoPage = 19, kInfoLength = 20, kInfoStarts = 21,
   // waits of the shared-prefix attention: a key/value stage, a query tile, the
-  // scores, the probabilities, the output tile, copies or MMAs in flight
+  // scores, the probabilities, the output tile, copies or MMAs in flight, the
+  // lists of segments, a slot's turn to issue
   kInfoAttnStage = 22, kInfoAttnQuery = 23, kInfoAttnScores = 24, kInfoAttnProbs = 25, kInfoAttnOut = 26,
-  kInfoAttnDrain = 27
+  kInfoAttnDrain = 27, kInfoAttnList = 28, kInfoAttnTurn = 29
 };
 
 // ----------------------------------------------------------------------------

@@ -26,9 +26,9 @@
 // timing.
 //
 // A CTA (one per SM): warp 0 loads query, key and value tiles by TMA (a page
-// is a box of its rows) into a ring of stages; warp 1 issues the MMAs, S = Q K^T
-// with both from shared memory, then O += P V with P from tensor memory; warps
-// 4..7 and 8..11 are the two slots' softmax, one row a thread.  While one
+// is a box of its rows) into a ring of stages; warps 1 and 2 issue the two
+// slots' MMAs, S = Q K^T with both from shared memory, then O += P V with P from
+// tensor memory; warps 4..7 and 8..11 are the slots' softmax, one row a thread.  While one
 // slot's softmax runs, the tensor cores work for the other.  Tensor memory is
 // full: two S tiles (P overwrites its own S) and two O tiles.
 //
@@ -52,6 +52,9 @@ constexpr int kAttnThreads = 384;    // 12 warps
 constexpr int kItemCost = 1;         // an item's fixed cost, in key tiles
 constexpr float kRescaleAt = 8.f;    // how far a tile's maximum may pass the reference (powers of two)
 constexpr int kAttnSmem = 232448;    // 227 KB
+// Registers a thread: 384 x 168 at launch, moved from warps 0..3 to the
+// softmax warps, which hold a row's 128 scores (128 x (104 + 2 x 200) = 384 x 168)
+constexpr int kRegsFew = 104, kRegsMany = 200;
 
 struct AttnParams {
   int T, B, Hq, Hkv, G, tpt;         // tpt: tokens of a row tile
@@ -66,27 +69,35 @@ struct AttnParams {
   // workspace
   int32_t* status;
   struct Plan* plan;
-  long long* first_unit;             // [B+1] units of a head's list before each request's
+  uint32_t* first_unit;              // [B+1] units of a head's list before each request's
   float2 *ml1, *ml2;                 // (reference, sum) of every part row, phases 1 and 2
   float *o1, *o2;                    // their fp32 rows
 };
 
+// A list of units cut into equal shares: share w holds the units [start(w),
+// start(w + 1)), the first `rest` shares one more than the others.  (Units are
+// counted in 32 bits: the entry point refuses work that could exceed them.)
+struct Shares {
+  uint32_t each, rest;
+  __host__ __device__ uint32_t start(uint32_t w) const { return w * each + (w < rest ? w : rest); }
+  __host__ __device__ uint32_t of(uint32_t u) const {  // the share that holds unit u
+    const uint32_t v = rest * (each + 1);
+    return u < v ? u / (each + 1) : rest + (u - v) / each;
+  }
+};
+__host__ __device__ inline Shares cut(uint32_t units, uint32_t shares) {
+  return Shares{units / shares, units % shares};
+}
+
 struct Plan {
-  long long per_head;                // phase 2 units of one head
+  uint32_t per_head;                 // phase 2 units of one head
   int prefix_tiles;
+  Shares s1, s2;
 };
 
 // ---------------------------------------------------------------- geometry
 __host__ __device__ inline int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __host__ __device__ inline int units_of(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
-
-// The share [start(w), start(w + 1)) of `shares` that holds unit u.
-__device__ __forceinline__ long long share_start(long long w, long long total, int shares) {
-  return w * total / shares;
-}
-__device__ __forceinline__ int share_of(long long u, long long total, int shares) {
-  return static_cast<int>(((u + 1) * shares - 1) / total);
-}
 
 // A length read on the device, held within its page table.
 __device__ __forceinline__ int held(int len, int pages, int page, int32_t* status) {
@@ -104,16 +115,17 @@ struct Request {
     return max(0, min(len, len - n + last));
   }
   __device__ int row_tiles(const AttnParams& p) const { return (n + p.tpt - 1) / p.tpt; }
-  __device__ long long units(const AttnParams& p) const {
-    long long u = 0;
+  __device__ uint32_t units(const AttnParams& p) const {
+    uint32_t u = 0;
     const int k = row_tiles(p);
-    if (!p.causal) return static_cast<long long>(k) * units_of(tiles_of(len));
+    if (!p.causal) return static_cast<uint32_t>(k) * units_of(tiles_of(len));
     for (int rt = 0; rt < k; ++rt) u += units_of(tiles_of(seen(p, rt)));
     return u;
   }
 };
 
-__device__ __forceinline__ Request read_request(const AttnParams& p, int b) {
+// (Not inlined, as what runs once a launch is bound by fetching its code.)
+__device__ __noinline__ Request read_request(const AttnParams& p, int b) {
   Request r;
   r.a = __ldg(p.q_start + b);
   const int z = __ldg(p.q_start + b + 1);
@@ -126,20 +138,22 @@ __device__ __forceinline__ Request read_request(const AttnParams& p, int b) {
   return r;
 }
 
-// One share's run through one item: row tile(s) against key tiles [j0, j1).
+// One share's run through one item: a slot's row tile against key tiles
+// [j0, j1).
 struct Segment {
-  int h, tok0, tok_end;      // key head, first token of the (first) row tile, end of valid tokens
+  int phase;                 // 0: the list has ended
+  int h, tok0, tok_end;      // key head, first token of the row tile, end of valid tokens
   int keys;                  // keys that any of its rows sees
   int own, lim0;             // own keys: token t sees min(keys, max(0, lim0 + t)) of them (causal)
-  const int32_t* pages;
   int j0, j1;
+  const int32_t* pages;
   long long part_row;        // part row of token tok0, head h * G
 };
 
-// Walks a share's segments; every role of a CTA runs its own copy.
+// Walks a share's segments.
 struct Walker {
   int phase, share;
-  long long left;  // units still to walk
+  uint32_t left;   // units still to walk
   int off;         // units of the current item before the share
   int h, i, rt;    // phase 1: h, pair i; phase 2: h, request i (-1: the prefix item), row tile rt
   Request rq;
@@ -148,21 +162,22 @@ struct Walker {
   // Phase 1, share c of p.ctas.
   __device__ void begin1(const AttnParams& p, int plen, int c) {
     phase = 1; share = c; prefix_len = plen; prefix_tiles = tiles_of(plen);
-    const long long per = units_of(prefix_tiles), total = per * p.pairs * p.Hkv;
-    const long long u0 = share_start(c, total, p.ctas);
-    left = share_start(c + 1, total, p.ctas) - u0;
+    const uint32_t per = units_of(prefix_tiles);
+    const Shares sh = cut(per * p.pairs * p.Hkv, p.ctas);
+    const uint32_t u0 = sh.start(c);
+    left = sh.start(c + 1) - u0;
     off = 0; h = i = rt = 0;
     if (left > 0) {
-      const long long item = u0 / per;
+      const uint32_t item = u0 / per;
       off = static_cast<int>(u0 - item * per);
       h = static_cast<int>(item / p.pairs);
-      i = static_cast<int>(item % p.pairs);
+      i = static_cast<int>(item) - h * p.pairs;
     }
   }
   // Phase 2, share w of 2 * p.ctas; the list position of its first unit was
   // found by the scan of the requests.
-  __device__ void begin2(const AttnParams& p, int plen, int w, long long units, int head, int request, int skip) {
-    phase = 2; share = w; prefix_len = plen; prefix_tiles = tiles_of(plen);
+  __device__ void begin2(const AttnParams& p, int w, uint32_t units, int head, int request, int skip) {
+    phase = 2; share = w;
     left = units; h = head; i = request; rt = 0; off = skip;
     if (left > 0 && i >= 0) rq = read_request(p, i);
   }
@@ -182,12 +197,13 @@ struct Walker {
         tiles = tiles_of(rq.seen(p, rt));
       }
       const int units = units_of(tiles);
-      const long long room = units - off;
+      const int room = units - off;
       if (room > 0) {
-        const long long take = left < room ? left : room;
+        const int take = left < static_cast<uint32_t>(room) ? static_cast<int>(left) : room;
+        s.phase = phase;
         s.h = h;
         s.j0 = max(off - kItemCost, 0);
-        s.j1 = static_cast<int>(off + take) - kItemCost;
+        s.j1 = off + take - kItemCost;
         if (prefix) {
           s.tok0 = (phase == 1 ? 2 * i : 2 * p.pairs) * p.tpt;
           s.tok_end = p.T;
@@ -201,7 +217,7 @@ struct Walker {
         }
         s.part_row = part_row(p, phase, h, s.tok0, !prefix, share);
         left -= take;
-        off += static_cast<int>(take);
+        off += take;
       }
       if (off >= units) {  // on to the next item (unless the share ends inside this one)
         off -= units;
@@ -236,39 +252,48 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, two 16-bit values a column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A B^T with A from shared or tensor memory (its rows lanes, two
+// 16-bit values a column).  A descriptor's upper word is a constant of its
+// layout and its lower word the address / 16 plus another constant, so that a
+// chain of MMAs costs its issuing thread one addition each.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, "
+      "%4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, "
-      "p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\ttcgen05.mma.cta_group::1."
+      "kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // Descriptor of a B operand whose N dimension is contiguous (value rows:
 // 64 columns of one key in 128 bytes, 128-byte swizzle): 8-key groups 1024
 // bytes apart, 64-column blocks kTile * 128 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((kTile * 128) >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);       // upper word of either layout
+constexpr uint32_t kDescLoK = 1u << 16;                                    // lower word, K contiguous (as sw128_desc)
+constexpr uint32_t kDescLoN = static_cast<uint32_t>((kTile * 128) >> 4) << 16;  // lower word, N contiguous
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
@@ -281,6 +306,30 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// The larger of three, and two fp32 operations in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -300,42 +349,35 @@ template <int D>
 struct Geometry {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQBufs = D == 64 ? 2 : 1;  // query tiles a slot
-  static constexpr int kStages = (kAttnSmem - 1024 - 2 * kQBufs * kTileBytes) / kTileBytes;
+  // 2 KB for the control words, 1 KB to align the tiles
+  static constexpr int kStages = (kAttnSmem - 2048 - 1024 - 2 * kQBufs * kTileBytes) / kTileBytes;
   static constexpr int kDynamic = 1024 + (2 * kQBufs + kStages) * kTileBytes;
 };
 
+// Key and value tiles land in a ring of stages in the order that the producer
+// chose; a slot's issuer finds its n-th tile through these.  At most 16 stages
+// are in use, so an entry is free again by the time it is written.
+constexpr int kSequence = 16;
+// A slot's segments pass from the planner to its 6 readers (producer, issuer,
+// four softmax warps) through a window of this many.
+constexpr int kSegments = 4;
+constexpr int kReaders = 6;
+
 struct Control {
   uint64_t q_full[2][2], q_empty[2][2];
-  uint64_t kv_full[16], kv_empty[16];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t kv_full[2][kSequence];  // per slot: its n-th tile has landed
+  uint64_t kv_empty[16];
+  uint64_t s_full[2], p_full[2], o_full[2], drain[2];
+  uint64_t turn[2];                // the slot may issue
+  int ended[2];                    // the slot's issuer takes no more turns
+  uint64_t seg_full[2][kSegments], seg_empty[2][kSegments];
+  Segment seg[2][kSegments];
+  int stage_of[2][kSequence];      // where the slot's n-th tile is
   uint32_t tmem;
   int abort_flag;
-  long long sums[kAttnThreads / 32];
-  long long units[2];  // phase 2 shares of the two slots
+  uint32_t sums[kAttnThreads / 32];
+  uint32_t units[2];               // phase 2 shares of the two slots, and where they begin
   int head[2], request[2], skip[2];
-  int prefix_len;
-};
-
-// A slot's place in its list of tiles.
-struct Cursor {
-  Walker w;
-  Segment s;
-  int j;
-  bool live;
-  __device__ void start(const AttnParams& p) {
-    live = w.next(p, s);
-    j = s.j0;
-  }
-  __device__ bool last() const { return j + 1 == s.j1; }
-  __device__ void step(const AttnParams& p) {
-    if (++j == s.j1) start(p);
-  }
-  __device__ int valid() const { return min(kTile, s.keys - j * kTile); }  // keys of the tile that some row sees
-};
-
-struct StageRing {
-  int stage = 0;
-  uint32_t phase = 0;
 };
 
 __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t parity, int32_t* status, int32_t info) {
@@ -344,8 +386,20 @@ __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t pa
   if ((threadIdx.x & 31) == 0) record_failure(status, &c.abort_flag, info);
   return false;
 }
+// The slot's n-th segment.
+__device__ __forceinline__ bool take(Control& c, int slot, int& n, Segment& s, int32_t* status) {
+  const int e = n % kSegments;
+  if (!warp_wait(c, &c.seg_full[slot][e], (n / kSegments) & 1, status, kInfoAttnList)) return false;
+  s = c.seg[slot][e];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&c.seg_empty[slot][e]);
+  ++n;
+  return true;
+}
+// Keys of tile j that some row of the segment sees.
+__device__ __forceinline__ int valid_keys(const Segment& s, int j) { return min(kTile, s.keys - j * kTile); }
 
-// ---------------------------------------------------------------- TMA producer (warp 0)
+// ---------------------------------------------------------------- TMA producer (one thread of warp 0)
 template <int D>
 struct Producer {
   using Geo = Geometry<D>;
@@ -354,105 +408,96 @@ struct Producer {
   uint8_t* q_mem;
   uint8_t* kv_mem;
   const CUtensorMap *tm_q, *tm_k, *tm_v;
-  StageRing ring;
-  int lane;
-  int q_fills[2];       // query tiles loaded so far, per slot
-  int kv_fills;         // stages filled so far
+  int box_rows;     // rows of a box: a page's, up to a tile's
+  Ring ring;
+  int q_fills[2];   // query tiles loaded so far, per slot
+  int kv_fills[2];  // tiles announced so far, per slot
 
-  // Page of this lane's box of tile j: boxes of min(page, 128) rows, a lane
-  // for each (box, 64-column half).
-  __device__ int page_id(const Segment& s, int j) {
-    const int box_rows = min(p.page, kTile);
-    const int box = lane / (D / 64);
-    const int key = j * kTile + box * box_rows;
-    if (box * box_rows >= kTile || key >= s.keys) return -1;
-    int pg = __ldg(s.pages + (key >> p.page_log2));
-    if (pg < 0 || pg >= p.n_pages) {
-      record_index(p.status, kInfoPage);
-      pg = p.n_pages;  // out of range: the copy fills zeros
-    }
-    return pg;
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t info) {
+    if (mbar_wait(bar, parity, &c.abort_flag)) return true;
+    record_failure(p.status, &c.abort_flag, info);
+    return false;
   }
-  __device__ bool load_kv(const CUtensorMap* tm, const Segment& s, int j, int pg) {
-    if (!warp_wait(c, &c.kv_empty[ring.stage], ring.phase ^ 1u, p.status, kInfoAttnStage)) return false;
-    const int box_rows = min(p.page, kTile);
-    const int valid = min(kTile, s.keys - j * kTile);
-    uint64_t* bar = &c.kv_full[ring.stage];
+  __device__ __forceinline__ bool take(int slot, int& n, Segment& s) {
+    const int e = n % kSegments;
+    if (!wait(&c.seg_full[slot][e], (n / kSegments) & 1, kInfoAttnList)) return false;
+    s = c.seg[slot][e];
+    mbar_arrive(&c.seg_empty[slot][e]);
+    ++n;
+    return true;
+  }
+  __device__ __forceinline__ int page_at(const Segment& s, int i) {
+    const int pg = __ldg(s.pages + i);
+    if (pg >= 0 && pg < p.n_pages) return pg;
+    record_index(p.status, kInfoPage);
+    return p.n_pages;  // out of range: the copy fills zeros
+  }
+  // The next tile of `slot` (in phase 1, of both: announced to slot 0): a box
+  // for each page and 64-column half.
+  __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment& s, int j, int slot) {
+    const int i0 = (j * kTile) >> p.page_log2, boxes = (valid_keys(s, j) + box_rows - 1) / box_rows;
+    int pg = page_at(s, i0);
+    if (!wait(&c.kv_empty[ring.stage], ring.phase ^ 1u, kInfoAttnStage)) return false;
+    const int entry = kv_fills[slot] % kSequence;
+    uint64_t* bar = &c.kv_full[slot][entry];
     uint8_t* dst = kv_mem + ring.stage * Geo::kTileBytes;
-    if (lane == 0) mbar_arrive_expect_tx(bar, ((valid + box_rows - 1) / box_rows) * box_rows * D * 2);
-    __syncwarp();
-    if (pg >= 0) {
-      const int box = lane / (D / 64), half = lane % (D / 64);
-      const int row = box * box_rows;
-      tma_load_4d(dst + half * (kTile * 128) + row * 128, tm, bar, half * 64, s.h, (j * kTile + row) & (p.page - 1),
-                  pg);
+    c.stage_of[slot][entry] = ring.stage;
+    mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
+    const int row = (j * kTile) & (p.page - 1);
+    for (int b = 0; b < boxes; ++b) {
+      const int next = b + 1 < boxes ? page_at(s, i0 + b + 1) : 0;
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half)
+        tma_load_4d(dst + half * (kTile * 128), tm, bar, half * 64, s.h, row, pg);
+      dst += box_rows * 128;
+      pg = next;
     }
-    ++kv_fills;
-    if (++ring.stage == Geo::kStages) { ring.stage = 0; ring.phase ^= 1u; }
+    ++kv_fills[slot];
+    ring.next(Geo::kStages);
     return true;
   }
-  // The query tile of a segment for `slot`: row tile `which` from its first.
-  __device__ bool load_q(const Segment& s, int slot, int which) {
+  __device__ __forceinline__ bool load_q(const Segment& s, int slot) {
     const int n = q_fills[slot]++, buf = n % Geo::kQBufs;
-    if (!warp_wait(c, &c.q_empty[slot][buf], ((n / Geo::kQBufs) & 1) ^ 1u, p.status, kInfoAttnQuery)) return false;
-    if (lane == 0) {
-      uint64_t* bar = &c.q_full[slot][buf];
-      uint8_t* dst = q_mem + (slot * Geo::kQBufs + buf) * Geo::kTileBytes;
-      mbar_arrive_expect_tx(bar, p.G * p.tpt * D * 2);
-      for (int half = 0; half < D / 64; ++half)
-        tma_load_4d(dst + half * (kTile * 128), tm_q, bar, half * 64, 0, s.h, s.tok0 + which * p.tpt);
-    }
-    __syncwarp();
+    if (!wait(&c.q_empty[slot][buf], ((n / Geo::kQBufs) & 1) ^ 1u, kInfoAttnQuery)) return false;
+    uint64_t* bar = &c.q_full[slot][buf];
+    uint8_t* dst = q_mem + (slot * Geo::kQBufs + buf) * Geo::kTileBytes;
+    mbar_arrive_expect_tx(bar, p.G * p.tpt * D * 2);
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half)
+      tma_load_4d(dst + half * (kTile * 128), tm_q, bar, half * 64, 0, s.h, s.tok0);
     return true;
   }
 
-  __device__ bool phase1() {
-    Cursor u;
-    u.w.begin1(p, c.prefix_len, blockIdx.x);
-    u.start(p);
-    if (!u.live) return true;
-    int pg = page_id(u.s, u.j);
-    if (!load_q(u.s, 0, 0) || !load_q(u.s, 1, 1) || !load_kv(tm_k, u.s, u.j, pg)) return false;
-    while (u.live) {
-      const Segment cur = u.s;
-      const int j = u.j, pg_cur = pg;
-      const bool fresh = u.last();
-      u.step(p);
-      if (u.live) pg = page_id(u.s, u.j);
-      if (!load_kv(tm_v, cur, j, pg_cur)) return false;
-      if (u.live) {
-        if (fresh && (!load_q(u.s, 0, 0) || !load_q(u.s, 1, 1))) return false;
-        if (!load_kv(tm_k, u.s, u.j, pg)) return false;
-      }
+  __device__ __forceinline__ bool run() {
+    Segment u[2];
+    int n[2] = {0, 0}, j[2] = {0, 0};
+    if (!take(0, n[0], u[0]) || !take(1, n[1], u[1])) return false;
+    // phase 1: the slots' segments differ in their row tile only
+    while (u[0].phase == 1) {
+      if (!load_q(u[0], 0) || !load_q(u[1], 1)) return false;
+      for (int i = u[0].j0; i < u[0].j1; ++i)
+        if (!load_kv(tm_k, u[0], i, 0) || !load_kv(tm_v, u[0], i, 0)) return false;
+      if (!take(0, n[0], u[0]) || !take(1, n[1], u[1])) return false;
     }
-    return true;
-  }
-  __device__ bool phase2() {
-    Cursor u[2];
-    int pg[2] = {-1, -1};
+    // phase 2: each slot its own; a slot's next keys follow its values
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      u[x].w.begin2(p, c.prefix_len, 2 * blockIdx.x + x, c.units[x], c.head[x], c.request[x], c.skip[x]);
-      u[x].start(p);
-      if (u[x].live) {
-        pg[x] = page_id(u[x].s, u[x].j);
-        if (!load_q(u[x].s, x, 0) || !load_kv(tm_k, u[x].s, u[x].j, pg[x])) return false;
+    for (int x = 0; x < 2; ++x)
+      if (u[x].phase) {
+        j[x] = u[x].j0;
+        if (!load_q(u[x], x) || !load_kv(tm_k, u[x], j[x], x)) return false;
       }
-    }
-    while (u[0].live || u[1].live) {
+    while (u[0].phase || u[1].phase) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (!u[x].live) continue;
-        const Segment cur = u[x].s;
-        const int j = u[x].j, pg_cur = pg[x];
-        const bool fresh = u[x].last();
-        u[x].step(p);
-        if (u[x].live) pg[x] = page_id(u[x].s, u[x].j);
-        if (!load_kv(tm_v, cur, j, pg_cur)) return false;
-        if (u[x].live) {
-          if (fresh && !load_q(u[x].s, x, 0)) return false;
-          if (!load_kv(tm_k, u[x].s, u[x].j, pg[x])) return false;
+        if (!u[x].phase) continue;
+        if (!load_kv(tm_v, u[x], j[x], x)) return false;
+        if (++j[x] == u[x].j1) {
+          if (!take(x, n[x], u[x])) return false;
+          if (!u[x].phase) continue;
+          j[x] = u[x].j0;
+          if (!load_q(u[x], x)) return false;
         }
+        if (!load_kv(tm_k, u[x], j[x], x)) return false;
       }
     }
     return true;
@@ -460,165 +505,176 @@ struct Producer {
   // Every copy that was issued has landed (also after a failure).
   __device__ void drain() {
     bool ok = true;
-    for (int st = 0; st < Geo::kStages; ++st) {
-      const int fills = kv_fills / Geo::kStages + (st < kv_fills % Geo::kStages ? 1 : 0);
-      if (fills > 0) ok &= mbar_wait(&c.kv_full[st], (fills - 1) & 1, nullptr);
-    }
-    for (int slot = 0; slot < 2; ++slot)
+    for (int slot = 0; slot < 2; ++slot) {
+      for (int e = 0; e < kSequence; ++e) {
+        const int fills = kv_fills[slot] / kSequence + (e < kv_fills[slot] % kSequence ? 1 : 0);
+        if (fills > 0) ok &= mbar_wait(&c.kv_full[slot][e], (fills - 1) & 1, nullptr);
+      }
       for (int b = 0; b < Geo::kQBufs; ++b) {
         const int fills = q_fills[slot] / Geo::kQBufs + (b < q_fills[slot] % Geo::kQBufs ? 1 : 0);
         if (fills > 0) ok &= mbar_wait(&c.q_full[slot][b], (fills - 1) & 1, nullptr);
       }
+    }
     if (!ok) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
   }
 };
 
-// ---------------------------------------------------------------- MMA issuer (warp 1)
+// ---------------------------------------------------------------- MMA issuers (warps 1 and 2, one a slot)
+// A slot's MMAs in the order S(0), O(0), S(1), O(1), ...: S(j + 1) overwrites
+// P(j), which O(j), issued just before by the same thread, has read.  The
+// slots take turns of O(j), S(j + 1): left to themselves their MMAs mix, both
+// slots' scores come at the same time, and the tensor cores idle while both
+// compute their probabilities.
 template <bool kBf16, int D>
 struct Issuer {
   using Geo = Geometry<D>;
   const AttnParams& p;
   Control& c;
-  uint8_t* q_mem;
-  uint8_t* kv_mem;
-  uint32_t tmem;
-  StageRing ring;
-  int lane;
-  int q_uses[2];         // query tiles taken so far, per slot
-  int q_buf[2];          // buffer of the slot's current query tile
-  uint32_t p_phase[2];   // parity of the slot's next P
+  uint32_t q_lo, kv_lo;  // lower descriptor words of the slot's first query tile and of stage 0
+  uint32_t s_tmem;       // the slot's S (and P); O lies 2 tiles further
+  int slot;
+  int q_uses, seen;      // query tiles and key/value tiles taken so far
+  uint32_t p_phase;      // parity of the slot's next P
+  uint32_t turn_phase;   // parity of the slot's next turn
+  bool mine;             // the first turn is slot 0's without a wait
+  bool alone;            // the other slot has ended
 
-  __device__ uint32_t idesc(int n) const { return kBf16 ? idesc_bf16(kTile, n) : idesc_f16(kTile, n); }
+  __device__ __forceinline__ uint32_t idesc(int n) const { return kBf16 ? idesc_bf16(kTile, n) : idesc_f16(kTile, n); }
 
-  __device__ bool wait_q(int slot) {
-    const int n = q_uses[slot]++;
-    q_buf[slot] = n % Geo::kQBufs;
-    if (!warp_wait(c, &c.q_full[slot][q_buf[slot]], (n / Geo::kQBufs) & 1, p.status, kInfoAttnQuery)) return false;
-    return true;
+  // The next tile announced to `sequence`: its stage, or -1.
+  __device__ __forceinline__ int wait_stage(int sequence) {
+    const int e = seen % kSequence;
+    if (!warp_wait(c, &c.kv_full[sequence][e], (seen / kSequence) & 1, p.status, kInfoAttnStage)) return -1;
+    ++seen;
+    return *reinterpret_cast<volatile int*>(&c.stage_of[sequence][e]);
   }
-  __device__ bool wait_stage(StageRing& at) {
-    at = ring;
-    if (++ring.stage == Geo::kStages) { ring.stage = 0; ring.phase ^= 1u; }
-    if (!warp_wait(c, &c.kv_full[at.stage], at.phase, p.status, kInfoAttnStage)) return false;
-    return true;
-  }
-  // S = Q K^T over the tile's keys (up to the next multiple of 16).
-  __device__ void scores(int slot, int stage, int valid, bool release_q) {
-    tc_fence_after();
-    if (lane == 0) {
-      const uint32_t id = idesc(((valid + 15) / 16) * 16);
-      const uint32_t a = smem_u32(q_mem + (slot * Geo::kQBufs + q_buf[slot]) * Geo::kTileBytes);
-      const uint32_t b = smem_u32(kv_mem + stage * Geo::kTileBytes);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t o = (ks / 4) * (kTile * 128) + (ks % 4) * 32;
-        mma_bf16(tmem + slot * kTile, sw128_desc(a + o), sw128_desc(b + o), id, ks > 0 ? 1u : 0u);
-      }
-      mma_commit(&c.s_full[slot]);
-      if (release_q) mma_commit(&c.q_empty[slot][q_buf[slot]]);
+  __device__ __forceinline__ bool begin_turn() {
+    if (alone) return true;
+    if (!mine) {
+      if (!warp_wait(c, &c.turn[slot], turn_phase, p.status, kInfoAttnTurn)) return false;
+      turn_phase ^= 1u;
     }
-    __syncwarp();
+    mine = false;
+    alone = *static_cast<volatile int*>(&c.ended[slot ^ 1]) != 0;
+    return true;
   }
-  // Value rows from the last key to the next multiple of 16: zeros.
-  __device__ void zero_tail(int stage, int valid) {
+  // kv_empty counts two users: both slots in phase 1, one (an arrival at once,
+  // the other with its last MMA) in phase 2.
+  __device__ __forceinline__ void release(int stage, bool both) {
+    if (!both) mbar_arrive(&c.kv_empty[stage]);
+    mma_commit(&c.kv_empty[stage]);
+  }
+  // Value rows from the last key to the next multiple of 16: zeros.  (In
+  // phase 1 both slots' issuers write the same zeros.)
+  __device__ void zero_tail(uint8_t* v, int valid) {
     const int end = ((valid + 15) / 16) * 16;
-    uint8_t* v = kv_mem + stage * Geo::kTileBytes;
-    for (int i = lane; i < (end - valid) * (D / 8); i += 32) {
+    for (int i = threadIdx.x & 31; i < (end - valid) * (D / 8); i += 32) {
       const int row = valid + i / (D / 8), ch = i % (D / 8);
       *reinterpret_cast<uint4*>(v + (ch / 8) * (kTile * 128) + row * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async();
     __syncwarp();
   }
-  // O (+)= P V.
-  __device__ bool outputs(int slot, int stage, int valid, bool first, bool last) {
-    if (!warp_wait(c, &c.p_full[slot], p_phase[slot], p.status, kInfoAttnProbs)) return false;
-    p_phase[slot] ^= 1u;
-    tc_fence_after();
-    if (lane == 0) {
-      const uint32_t id = idesc(D) | (1u << 16);  // B: N-major
-      const uint32_t b = smem_u32(kv_mem + stage * Geo::kTileBytes);
-      const int steps = (valid + 15) / 16;
-      for (int ks = 0; ks < steps; ++ks)
-        mma_ts(tmem + 2 * kTile + slot * kTile, tmem + slot * kTile + ks * 8, sw128_desc_mn(b + ks * 2048), id,
-               (!first || ks > 0) ? 1u : 0u);
-      if (last) mma_commit(&c.o_full[slot]);
+  // One tile's operands of S, all waited for: its query buffer and stage.
+  struct Keys {
+    int q_buf, stage, valid;
+    bool both, last;  // both slots' stage; the segment's last tile
+  };
+  __device__ __forceinline__ bool wait_keys(Keys& k, const Segment& s, int j) {
+    k.both = s.phase == 1;  // phase 1's tiles are announced to slot 0
+    k.valid = valid_keys(s, j);
+    k.last = j + 1 == s.j1;
+    if (j == s.j0) {
+      if (!warp_wait(c, &c.q_full[slot][q_uses % Geo::kQBufs], (q_uses / Geo::kQBufs) & 1, p.status, kInfoAttnQuery))
+        return false;
+      ++q_uses;
     }
-    __syncwarp();
-    return true;
+    k.q_buf = (q_uses - 1) % Geo::kQBufs;
+    k.stage = wait_stage(k.both ? 0 : slot);
+    return k.stage >= 0;
   }
-  __device__ void release(int stage) {
-    if (lane == 0) mma_commit(&c.kv_empty[stage]);
-    __syncwarp();
+  // S = Q K^T over the tile's keys (up to the next multiple of 16), by one
+  // thread.  The turn ends while the last products are still queued: the other
+  // slot's follow them without a gap.
+  __device__ __forceinline__ void scores(const Keys& k) {
+    const uint32_t id = idesc(((k.valid + 15) / 16) * 16);
+    const uint32_t a = kDescLoK + q_lo + k.q_buf * (Geo::kTileBytes / 16);
+    const uint32_t b = kDescLoK + kv_lo + k.stage * (Geo::kTileBytes / 16);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t o = (ks / 4) * (kTile * 128 / 16) + (ks % 4) * 2;
+      mma_ss(s_tmem, a + o, kDescHi, b + o, kDescHi, id, ks > 0 ? 1u : 0u);
+      if (ks == D / 16 - 4 && !alone) mbar_arrive(&c.turn[slot ^ 1]);
+    }
+    mma_commit(&c.s_full[slot]);
+    release(k.stage, k.both);
+    if (k.last) mma_commit(&c.q_empty[slot][k.q_buf]);
+  }
+  // O (+)= P V, by one thread.
+  __device__ __forceinline__ void outputs(const Keys& k, int stage, bool first) {
+    const uint32_t id = idesc(D) | (1u << 16);  // B: N-major
+    const uint32_t b = kDescLoN + kv_lo + stage * (Geo::kTileBytes / 16);
+    const uint32_t d = s_tmem + 2 * kTile;
+    const int steps = (k.valid + 15) / 16;
+    if (steps == kTile / 16) {
+#pragma unroll
+      for (int ks = 0; ks < kTile / 16; ++ks)
+        mma_ts(d, s_tmem + ks * 8, b + ks * (2048 / 16), kDescHi, id, ks > 0 ? 1u : first ? 0u : 1u);
+    } else {
+      for (int ks = 0; ks < steps; ++ks)
+        mma_ts(d, s_tmem + ks * 8, b + ks * (2048 / 16), kDescHi, id, ks > 0 || !first ? 1u : 0u);
+    }
+    if (k.last) mma_commit(&c.o_full[slot]);
+    release(stage, k.both);
   }
 
-  __device__ bool phase1() {
-    Cursor u;
-    u.w.begin1(p, c.prefix_len, blockIdx.x);
-    u.start(p);
-    if (!u.live) return true;
-    StageRing k, v;
-    if (!wait_stage(k)) return false;
-    for (int x = 0; x < 2; ++x) {
-      if (!wait_q(x)) return false;
-      scores(x, k.stage, u.valid(), u.last());
-    }
-    release(k.stage);
-    while (u.live) {
-      const bool first = u.j == u.s.j0, last = u.last();
-      const int valid = u.valid();
-      u.step(p);
-      if (!wait_stage(v)) return false;
-      if (valid % 16) zero_tail(v.stage, valid);
-      if (!outputs(0, v.stage, valid, first, last)) return false;
-      if (u.live) {
-        if (last && !wait_q(0)) return false;
-        if (!wait_stage(k)) return false;
-        scores(0, k.stage, u.valid(), u.last());
+  __device__ __forceinline__ bool walk(uint8_t* kv_mem) {
+    Segment u;
+    Keys cur, next;
+    int n = 0;
+    if (!take(c, slot, n, u, p.status)) return false;
+    if (u.phase == 0) return true;
+    int j = u.j0;
+    if (!wait_keys(cur, u, j) || !begin_turn()) return false;
+    tc_fence_after();
+    if (elect()) scores(cur);
+    __syncwarp();
+    while (true) {
+      // all of the turn's operands are there before it begins
+      const int stage = wait_stage(cur.both ? 0 : slot);
+      if (stage < 0) return false;
+      const bool first = j == u.j0;
+      if (cur.valid % 16) zero_tail(kv_mem + stage * Geo::kTileBytes, cur.valid);
+      ++j;
+      if (cur.last) {
+        if (!take(c, slot, n, u, p.status)) return false;
+        j = u.j0;
+        if (cur.both && u.phase != 1 && slot == 1) seen = 0;
       }
-      if (!outputs(1, v.stage, valid, first, last)) return false;
-      release(v.stage);
-      if (u.live) {
-        if (last && !wait_q(1)) return false;
-        scores(1, k.stage, u.valid(), u.last());
-        release(k.stage);
+      const bool more = u.phase != 0;
+      if (more && !wait_keys(next, u, j)) return false;
+      // the turn first: it usually comes while the probabilities are computed
+      if (!begin_turn()) return false;
+      if (!warp_wait(c, &c.p_full[slot], p_phase, p.status, kInfoAttnProbs)) return false;
+      p_phase ^= 1u;
+      tc_fence_after();
+      if (elect()) {
+        outputs(cur, stage, first);
+        if (more) scores(next);
       }
+      __syncwarp();
+      if (!more) return true;
+      cur = next;
     }
-    return true;
   }
-  __device__ bool phase2() {
-    Cursor u[2];
-    StageRing at;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      u[x].w.begin2(p, c.prefix_len, 2 * blockIdx.x + x, c.units[x], c.head[x], c.request[x], c.skip[x]);
-      u[x].start(p);
-      if (u[x].live) {
-        if (!wait_q(x) || !wait_stage(at)) return false;
-        scores(x, at.stage, u[x].valid(), u[x].last());
-        release(at.stage);
-      }
+  __device__ __forceinline__ void run(uint8_t* kv_mem) {
+    walk(kv_mem);
+    // the turn, if it is this slot's or comes to it, is the other's from here on
+    if (elect()) {
+      *static_cast<volatile int*>(&c.ended[slot]) = 1;
+      mbar_arrive(&c.turn[slot ^ 1]);
     }
-    while (u[0].live || u[1].live) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!u[x].live) continue;
-        const bool first = u[x].j == u[x].s.j0, last = u[x].last();
-        const int valid = u[x].valid();
-        u[x].step(p);
-        if (!wait_stage(at)) return false;
-        if (valid % 16) zero_tail(at.stage, valid);
-        if (!outputs(x, at.stage, valid, first, last)) return false;
-        release(at.stage);
-        if (u[x].live) {
-          if (last && !wait_q(x)) return false;
-          if (!wait_stage(at)) return false;
-          scores(x, at.stage, u[x].valid(), u[x].last());
-          release(at.stage);
-        }
-      }
-    }
-    return true;
+    __syncwarp();
   }
 };
 
@@ -634,15 +690,20 @@ struct Softmax {
   __device__ bool wait(uint64_t* bar, uint32_t parity, int32_t info) {
     return warp_wait(c, bar, parity, p.status, info);
   }
-  // One segment: rows of row tile `which` from the segment's first.
-  __device__ bool run(const Segment& s, int which, float2* ml, float* o) {
-    const int tok = s.tok0 + which * p.tpt + row / p.G;
+  __device__ __forceinline__ bool segment(const Segment& s) {
+    const int tok = s.tok0 + row / p.G;
     const bool valid_row = row < p.tpt * p.G && tok < s.tok_end;
     const int limit = s.own ? max(0, min(s.keys, s.lim0 + tok)) : s.keys;
+    // a warp without a valid row (a block of few tokens) only keeps step
+    const bool idle = !__any_sync(0xffffffffu, valid_row);
     float m = -INFINITY, l = 0.f;
     for (int j = s.j0; j < s.j1; ++j) {
       if (!wait(&c.s_full[slot], s_phase, kInfoAttnScores)) return false;
       s_phase ^= 1u;
+      if (idle) {
+        mbar_arrive(&c.p_full[slot]);
+        continue;
+      }
       tc_fence_after();
       uint32_t x[kTile];
 #pragma unroll
@@ -656,7 +717,8 @@ struct Softmax {
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
+      for (int i = 0; i < kTile; i += 2)
+        top[(i / 2) % 4] = max3(top[(i / 2) % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
       const bool move = mt > m + kRescaleAt;  // also from -infinity
       if (__any_sync(0xffffffffu, move)) {
@@ -667,29 +729,33 @@ struct Softmax {
         if (j > s.j0) {
           // the slot's earlier products are complete: the same commit that
           // announced this S followed them
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t y[32];
-            tmem_ld32(o_tmem + 32 * i, y);
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t y[16];
+            tmem_ld16(o_tmem + 16 * i, y);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
-            tmem_st32(o_tmem + 32 * i, y);
+            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * a);
+            tmem_st16(o_tmem + 16 * i, y);
           }
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const unsigned long long scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
+      unsigned long long sum[2] = {0ull, 0ull};  // two zeros each
 #pragma unroll
       for (int i = 0; i < kTile / 2; ++i) {
-        const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), p.scale_log2, -base));
-        const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), p.scale_log2, -base));
-        sum[i % 2] += e0;
-        sum[2 + i % 2] += e1;
+        float e0, e1;
+        unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, base2), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        sum[i % 2] = add2(sum[i % 2], pair(e0, e1));
         x[i] = pack2<kBf16>(e0, e1);
-        if (i % 32 == 31) tmem_st32(s_tmem + (i - 31), x + (i - 31));
+        if (i % 16 == 15) tmem_st16(s_tmem + (i - 15), x + (i - 15));
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float s0, s1;
+      unpair(add2(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&c.p_full[slot]);
@@ -697,7 +763,8 @@ struct Softmax {
     if (!wait(&c.o_full[slot], o_phase, kInfoAttnOut)) return false;
     o_phase ^= 1u;
     tc_fence_after();
-    const long long r = s.part_row + static_cast<long long>(which) * p.tpt * p.G + row;
+    const long long r = s.part_row + row;
+    float* o = s.phase == 1 ? p.o1 : p.o2;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t y[32];
@@ -711,71 +778,138 @@ struct Softmax {
                                __uint_as_float(y[4 * k + 3]));
       }
     }
-    if (valid_row) ml[r] = make_float2(m, l);
+    if (valid_row) (s.phase == 1 ? p.ml1 : p.ml2)[r] = make_float2(m, l);
     return true;
+  }
+  __device__ __forceinline__ void run() {
+    Segment s;
+    int n = 0;
+    while (take(c, slot, n, s, p.status) && s.phase != 0)
+      if (!segment(s)) return;
   }
 };
 
-// The list position of both slots' phase 2 shares: a scan over the requests'
-// units.  CTA 0 also leaves the scan for merge_kernel.
-__device__ void find_shares(const AttnParams& p, Control& c, int plen) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kAttnThreads / 32;
-  long long mine = 0, cost0 = 0;
-  for (int b = tid; b < p.B; b += kAttnThreads) {
-    const long long u = read_request(p, b).units(p);
+// ---------------------------------------------------------------- planner (warp 3)
+constexpr int kScanAlone = 32;  // up to this many requests one warp scans them, else the whole CTA
+
+// Both slots' places in the phase 2 list: a scan over the requests' units by
+// kThreads threads (a warp, or the CTA).  CTA 0 also leaves it for
+// merge_kernel.
+template <int kThreads>
+__device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int plen) {
+  const int lane = threadIdx.x & 31;
+  const int tid = kThreads == 32 ? lane : threadIdx.x, warp = kThreads == 32 ? 0 : threadIdx.x >> 5;
+  constexpr int kWarps = kThreads / 32;
+  const uint32_t lead = p.left ? units_of(tiles_of(plen)) : 0;  // the prefix item comes first
+  const auto sync = [] { if (kThreads == 32) __syncwarp(); else __syncthreads(); };
+  uint32_t mine = 0, cost0 = 0;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const uint32_t u = read_request(p, b).units(p);
     if (b == tid) cost0 = u;
     mine += u;
   }
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) c.sums[warp] = mine;
-  __syncthreads();
-  long long per_head = p.left ? units_of(tiles_of(plen)) : 0;
-  const long long lead = per_head;
-  for (int w = 0; w < kWarps; ++w) per_head += c.sums[w];
-  __syncthreads();
-  const long long total = per_head * p.Hkv;
-  long long rem[2];
-  for (int x = 0; x < 2; ++x) {
-    const long long u0 = share_start(2 * blockIdx.x + x, total, 2 * p.ctas);
-    const long long units = share_start(2 * blockIdx.x + x + 1, total, 2 * p.ctas) - u0;
-    const int head = per_head > 0 ? static_cast<int>(u0 / per_head) : 0;
-    rem[x] = units > 0 ? u0 - head * per_head - lead : -1;
-    if (tid == 0) {
-      c.units[x] = units;
-      c.head[x] = head;
-      if (rem[x] < 0) { c.request[x] = -1; c.skip[x] = units > 0 ? static_cast<int>(rem[x] + lead) : 0; }
-    }
+  uint32_t all = __reduce_add_sync(0xffffffffu, mine);
+  if (kThreads != 32) {
+    if (lane == 0) c.sums[warp] = all;
+    sync();
+    all = 0;
+    for (int w = 0; w < kWarps; ++w) all += c.sums[w];
+    sync();
   }
+  const uint32_t per_head = lead + all;
+  const Shares sh = cut(per_head * p.Hkv, 2 * p.ctas);
   if (blockIdx.x == 0 && tid == 0) {
     p.plan->per_head = per_head;
     p.plan->prefix_tiles = tiles_of(plen);
+    p.plan->s1 = cut(units_of(tiles_of(plen)) * p.pairs * p.Hkv, p.ctas);
+    p.plan->s2 = sh;
   }
-  long long base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
-    const int b = b0 + tid;
-    const long long u = b < p.B ? (b0 == 0 ? cost0 : read_request(p, b).units(p)) : 0;
-    long long inc = u;
+  // where each slot's share begins in its head's list; below `lead`: inside
+  // the prefix item
+  uint32_t at[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t u0 = sh.start(2 * blockIdx.x + x), units = sh.start(2 * blockIdx.x + x + 1) - u0;
+    const uint32_t head = units > 0 ? u0 / per_head : 0;
+    at[x] = units > 0 ? u0 - head * per_head : 0;
+    if (tid == 0) {
+      c.units[x] = units;
+      c.head[x] = static_cast<int>(head);
+      if (units == 0 || at[x] < lead) { c.request[x] = -1; c.skip[x] = static_cast<int>(at[x]); }
+    }
+    if (units == 0) at[x] = 0xffffffffu;
+  }
+  uint32_t base = lead;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    uint32_t own = cost0;
+    if (b0 > 0) own = b0 + tid < p.B ? read_request(p, b0 + tid).units(p) : 0;
+    uint32_t inc = own;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) c.sums[warp] = inc;
-    __syncthreads();
-    long long before = base, all = base;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += c.sums[w];
-      all += c.sums[w];
+    uint32_t first = base + inc - own;
+    if (kThreads == 32) {
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    } else {
+      if (lane == 31) c.sums[warp] = inc;
+      sync();
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) first += c.sums[w];
+        base += c.sums[w];
+      }
+      sync();
     }
-    const long long first = before + inc - u;
+    const int b = b0 + tid;
+#pragma unroll
     for (int x = 0; x < 2; ++x)
-      if (b < p.B && rem[x] >= first && rem[x] < first + u) {
+      if (at[x] >= first && at[x] - first < own) {
         c.request[x] = b;
-        c.skip[x] = static_cast<int>(rem[x] - first);
+        c.skip[x] = static_cast<int>(at[x] - first);
       }
     if (blockIdx.x == 0 && b < p.B) p.first_unit[b] = first;
-    base = all;
-    __syncthreads();
+  }
+  sync();
+}
+
+// Hands a slot's list over, a segment whenever its readers have made room.
+// Lane x is slot x: neither slot waits for the other.
+__device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int slot, int plen) {
+  Walker w;
+  Segment s;
+  int n = 0;
+  w.begin1(p, plen, blockIdx.x);
+  long long t0 = clock64();
+  bool have = false;
+  while (true) {
+    if (!have) {
+      while (!w.next(p, s)) {
+        if (w.phase == 2) { s.phase = 0; break; }
+        w.begin2(p, 2 * blockIdx.x + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
+      }
+      if (s.phase == 1 && slot == 1) {  // the pair's second row tile
+        s.tok0 += p.tpt;
+        s.part_row += static_cast<long long>(p.tpt) * p.G;
+      }
+      have = true;
+    }
+    const int e = n % kSegments;
+    if (mbar_test_wait(&c.seg_empty[slot][e], ((n / kSegments) & 1) ^ 1u)) {
+      c.seg[slot][e] = s;
+      mbar_arrive(&c.seg_full[slot][e]);
+      if (s.phase == 0) return;
+      ++n;
+      have = false;
+      t0 = clock64();
+    } else {
+      if (*static_cast<volatile int*>(&c.abort_flag)) return;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        record_failure(p.status, &c.abort_flag, kInfoAttnList);
+        return;
+      }
+      __nanosleep(64);
+    }
   }
 }
 
@@ -797,9 +931,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], kTile);
       mbar_init(&c.o_full[s], 1);
+      mbar_init(&c.turn[s], 1);
+      c.ended[s] = 0;
     }
-    for (int s = 0; s < Geo::kStages; ++s) { mbar_init(&c.kv_full[s], 1); mbar_init(&c.kv_empty[s], 1); }
-    mbar_init(&c.drain, 1);
+    for (int s = 0; s < 2 * kSegments; ++s) {
+      mbar_init(&c.seg_full[s / kSegments][s % kSegments], 1);
+      mbar_init(&c.seg_empty[s / kSegments][s % kSegments], kReaders);
+    }
+    for (int s = 0; s < kSequence; ++s) { mbar_init(&c.kv_full[0][s], 1); mbar_init(&c.kv_full[1][s], 1); }
+    for (int s = 0; s < Geo::kStages; ++s) mbar_init(&c.kv_empty[s], 2);
+    mbar_init(&c.drain[0], 1);
+    mbar_init(&c.drain[1], 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -811,37 +953,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   griddep_wait();  // what the previous kernel on the stream wrote is visible
   const int plen = p.prefix_cap > 0 ? held(__ldg(p.prefix_len), p.prefix_cap, p.page, p.status) : 0;
-  if (tid == 0) c.prefix_len = plen;
-  find_shares(p, c, plen);
+  if (p.B > kScanAlone) find_shares<kAttnThreads>(p, c, plen);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
 
-  if (warp == 0) {
-    Producer<D> r{p, c, q_mem, kv_mem, &tm_q, &tm_k, &tm_v, StageRing(), lane, {0, 0}, 0};
-    if (r.phase1()) r.phase2();
-    if (lane == 0) r.drain();
-  } else if (warp == 1) {
-    Issuer<kBf16, D> r{p, c, q_mem, kv_mem, tmem, StageRing(), lane, {0, 0}, {0, 0}, {0, 0}};
-    if (r.phase1()) r.phase2();
-    // every MMA issued above has completed once `drain` flips
-    if (lane == 0) {
-      mma_commit(&c.drain);
-      if (!mbar_wait(&c.drain, 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0) {
+      if (elect()) {
+        Producer<D> r{p, c, q_mem, kv_mem, &tm_q, &tm_k, &tm_v, min(p.page, kTile), Ring(), {0, 0}, {0, 0}};
+        r.run();
+        r.drain();
+      }
+    } else if (warp <= 2) {
+      const int slot = warp - 1;
+      Issuer<kBf16, D> r{p, c, smem_u32(q_mem + slot * Geo::kQBufs * Geo::kTileBytes) >> 4, smem_u32(kv_mem) >> 4,
+                         tmem + slot * kTile, slot, 0, 0, 0, 0u, slot == 0, false};
+      r.run(kv_mem);
+      // every MMA issued above has completed once `drain` flips
+      if (elect()) {
+        mma_commit(&c.drain[slot]);
+        if (!mbar_wait(&c.drain[slot], 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
+      }
+    } else if (warp == 3) {
+      if (p.B <= kScanAlone) find_shares<32>(p, c, plen);
+      if (lane < 2) hand_list(p, c, lane, plen);
     }
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
     const int slot = (warp - 4) / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     Softmax<kBf16, D> r{p, c, slot, (warp % 4) * 32 + lane, tmem + slot * kTile + lanes,
                         tmem + 2 * kTile + slot * kTile + lanes, 0, 0};
-    Walker w;
-    Segment s;
-    bool ok = true;
-    w.begin1(p, plen, blockIdx.x);
-    while (ok && w.next(p, s)) ok = r.run(s, slot, p.ml1, p.o1);
-    w.begin2(p, plen, 2 * blockIdx.x + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
-    while (ok && w.next(p, s)) ok = r.run(s, 0, p.ml2, p.o2);
+    r.run();
   }
   griddep_launch_dependents();
   __syncwarp();
@@ -854,90 +1000,136 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining a row's parts
-// One warp per (token, head).  A row's parts are the shares that hold tiles of
-// its items: consecutive shares, those without units left out.
-template <bool kBf16, int D>
+// kWarps warps per (token, head).  A row's parts are the shares that hold
+// tiles of its items: consecutive shares.  Their rows are independent loads, so a part costs little more than its bytes; the
+// fewer rows a call has, the more parts each has, and the more warps take it.
+struct Parts {
+  const float2* ml;
+  const float* o;
+  long long row;  // part row of share 0
+  int first, count, stride;
+  __device__ long long at(int i) const { return row + static_cast<long long>(stride) * (first + i); }
+};
+
+template <bool kBf16, int D, int kWarps>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kPer = D / 32;
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * 4ll + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.T) * p.Hq) return;
+  __shared__ float2 ml_all[4];
+  __shared__ float acc_all[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_warp = warp % kWarps;
+  const long long row = blockIdx.x * (4ll / kWarps) + warp / kWarps;
+  if (row >= static_cast<long long>(p.T) * p.Hq) return;  // whole blocks where kWarps is 4
   const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row % p.Hq), h = hq / p.G, g = hq % p.G;
-  const long long per_head = p.plan->per_head, total2 = per_head * p.Hkv;
+  griddep_wait();
+  const uint32_t per_head = p.plan->per_head;
   const int ptiles = p.plan->prefix_tiles;
+  const Shares s1 = p.plan->s1, s2 = p.plan->s2;
 
-  // up to two runs of parts: the prefix item's, the request's
-  const float2* ml[2] = {nullptr, nullptr};
-  const float* o[2] = {nullptr, nullptr};
-  long long first_row[2] = {0, 0}, total[2] = {1, 1};
-  int first[2] = {0, 0}, last[2] = {-1, -1}, shares[2] = {1, 1}, stride[2] = {0, 0};
-  // the request of token t: the last b with q_start[b] <= t
-  int lo = 0, hi = p.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(p.q_start + mid) <= t) lo = mid + 1; else hi = mid;
+  // the request of token t: the last b with q_start[b] <= t, 32 starts a step
+  int lo = 0, n = p.B;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lo + min(n, (lane + 1) * step) - 1;  // last of this lane's group
+    const bool le = lane * step < n && __ldg(p.q_start + i) <= t;
+    const int groups = __popc(__ballot_sync(0xffffffffu, le));  // whole groups at or before t
+    lo += min(n, groups * step);
+    n = min(step, n - min(n, groups * step));
+    if (step == 1) break;
+    n = n > 0 ? n - 1 : 0;  // the last of the next group is past t
   }
   const int b = lo - 1;
   Request rq;
-  rq.n = 0;
+  rq.a = rq.n = rq.len = 0;
   if (b >= 0) rq = read_request(p, b);
   const bool owned = b >= 0 && t >= rq.a && t < rq.a + rq.n;
+  Parts run[2];  // the prefix item's parts, the request's
+  run[0].count = run[1].count = 0;
   if (owned && ptiles > 0) {
     const int rt = t / p.tpt;
-    const long long per = units_of(ptiles);
-    if (rt < 2 * p.pairs) {
-      total[0] = per * p.pairs * p.Hkv; shares[0] = p.ctas; stride[0] = 2 * kTile;
-      const long long u = (static_cast<long long>(h) * p.pairs + rt / 2) * per + kItemCost;
-      first[0] = share_of(u, total[0], shares[0]);
-      last[0] = share_of(u + ptiles - 1, total[0], shares[0]);
-      first_row[0] = Walker::part_row(p, 1, h, t, false, 0) + g;
-      ml[0] = p.ml1; o[0] = p.o1;
-    } else {
-      total[0] = total2; shares[0] = 2 * p.ctas; stride[0] = kTile;
-      const long long u = h * per_head + kItemCost;
-      first[0] = share_of(u, total2, shares[0]);
-      last[0] = share_of(u + ptiles - 1, total2, shares[0]);
-      first_row[0] = Walker::part_row(p, 2, h, t, false, 0) + g;
-      ml[0] = p.ml2; o[0] = p.o2;
-    }
+    const bool paired = rt < 2 * p.pairs;
+    Parts& r = run[0];
+    r.ml = paired ? p.ml1 : p.ml2;
+    r.o = paired ? p.o1 : p.o2;
+    r.stride = paired ? 2 * kTile : kTile;
+    const Shares sh = paired ? s1 : s2;
+    const uint32_t u = (paired ? (h * p.pairs + rt / 2) * units_of(ptiles) : h * per_head) + kItemCost;
+    r.first = sh.of(u);
+    r.count = sh.of(u + ptiles - 1) - r.first + 1;
+    r.row = Walker::part_row(p, paired ? 1 : 2, h, t, false, 0) + g;
   }
   if (owned) {
     const int rt = (t - rq.a) / p.tpt;
     const int tiles = tiles_of(rq.seen(p, rt));
     if (tiles > 0) {
-      long long u = h * per_head + (p.left ? units_of(ptiles) : 0) + p.first_unit[b] + kItemCost;
+      uint32_t u = h * per_head + p.first_unit[b] + kItemCost;
       for (int i = 0; i < rt; ++i) u += units_of(tiles_of(rq.seen(p, i)));
-      total[1] = total2; shares[1] = 2 * p.ctas; stride[1] = kTile;
-      first[1] = share_of(u, total2, shares[1]);
-      last[1] = share_of(u + tiles - 1, total2, shares[1]);
-      first_row[1] = Walker::part_row(p, 2, h, t, true, 0) + g;
-      ml[1] = p.ml2; o[1] = p.o2;
+      Parts& r = run[1];
+      r.ml = p.ml2; r.o = p.o2; r.stride = kTile;
+      r.first = s2.of(u);
+      r.count = s2.of(u + tiles - 1) - r.first + 1;
+      r.row = Walker::part_row(p, 2, h, t, true, 0) + g;
     }
   }
-  float m = -INFINITY;
-  for (int k = 0; k < 2; ++k)
-    for (int w = first[k] + lane; w <= last[k]; w += 32)
-      if (share_start(w + 1, total[k], shares[k]) > share_start(w, total[k], shares[k]))
-        m = fmaxf(m, ml[k][first_row[k] + static_cast<long long>(stride[k]) * w].x);
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[kPer];
+  float m = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
   for (int k = 0; k < 2; ++k)
-    for (int w = first[k]; w <= last[k]; ++w) {
-      if (share_start(w + 1, total[k], shares[k]) <= share_start(w, total[k], shares[k])) continue;
-      const long long r = first_row[k] + static_cast<long long>(stride[k]) * w;
-      const float2 part = ml[k][r];
-      const float a = ex2(part.x - base);
-      l += part.y * a;
-      const float* src = o[k] + r * D + lane * kPer;
-      for (int i = 0; i < kPer; ++i) acc[i] += a * src[i];
+    for (int i0 = 0; i0 < run[k].count; i0 += 32 * kWarps) {
+      // lane i: this warp's i-th part of the chunk
+      const int i = i0 + lane * kWarps + part_warp;
+      const long long at = i < run[k].count ? run[k].at(i) : -1;
+      const float2 ml = at >= 0 ? run[k].ml[at] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1;
+      const float old = ex2(m - base), mine = ex2(ml.x - base);
+      m = m1;
+      float sum = mine * ml.y;
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = l * old + sum;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) acc[x] *= old;
+      const int count = min(32, (run[k].count - i0 - part_warp + kWarps - 1) / kWarps);
+#pragma unroll 8
+      for (int x = 0; x < count; ++x) {
+        const long long r = __shfl_sync(0xffffffffu, at, x);
+        const float a = __shfl_sync(0xffffffffu, mine, x);
+        if (r >= 0) {
+          const float* src = run[k].o + r * D + lane * kPer;
+          if (kPer == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            acc[0] += a * v.x; acc[1] += a * v.y; acc[kPer - 2] += a * v.z; acc[kPer - 1] += a * v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            acc[0] += a * v.x; acc[1] += a * v.y;
+          }
+        }
+      }
     }
+  if (kWarps > 1) {
+    if (lane == 0) ml_all[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc_all[warp][lane * kPer + i] = acc[i];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_all[w].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = ex2(ml_all[w].x - base);
+      l += a * ml_all[w].y;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += a * acc_all[w][lane * kPer + i];
+    }
+  }
+  const float base = m == -INFINITY ? 0.f : m;
   const float r = l > 0.f ? 1.f / l : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kPer);
-  for (int i = 0; i < kPer / 2; ++i)
-    dst[i] = l == 0.f ? 0u : pack2<kBf16>(acc[2 * i] * r, acc[2 * i + 1] * r);
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) dst[i] = l == 0.f ? 0u : pack2<kBf16>(acc[2 * i] * r, acc[2 * i + 1] * r);
   if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -969,7 +1161,7 @@ AttnLayout attn_layout(int T, int B, int Hq, int Hkv, int D, int ctas) {
   const size_t rows2 = (static_cast<size_t>(T) + l0) * Hq + 2ull * kTile * ctas;
   size_t o = kWsHeaderBytes;
   L.o_plan = o; o += kWsAlign;
-  L.o_first = o; o += ws_align_up(8 * (static_cast<size_t>(B) + 1));
+  L.o_first = o; o += ws_align_up(4 * (static_cast<size_t>(B) + 1));
   L.o_ml1 = o; o += ws_align_up(8 * rows1);
   L.o_ml2 = o; o += ws_align_up(8 * rows2);
   L.o_o1 = o; o += ws_align_up(4 * rows1 * D);
@@ -1003,9 +1195,12 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   launch_config(&cfg, &attr, static_cast<unsigned>(p.ctas), kAttnThreads, Geometry<D>::kDynamic, s);
   e = cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kBf16, D>, tm_q, tm_k, tm_v, p);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.T) * p.Hq + 3) / 4);
-  launch_config(&cfg, &attr, grid, 128, 0, s);
-  return cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D>, p);
+  // four warps a row while the rows leave the SMs room for them
+  const long long rows = static_cast<long long>(p.T) * p.Hq;
+  const bool wide = rows <= 32ll * p.ctas;
+  launch_config(&cfg, &attr, static_cast<unsigned>(wide ? rows : (rows + 3) / 4), 128, 0, s);
+  return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 4>, p)
+              : cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 1>, p);
 }
 
 }  // namespace
@@ -1037,6 +1232,12 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
       static_cast<long long>(table_width) * page_size > MOE_MAX_KEYS)
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
+  // units of both phases' lists, at most, in 31 bits
+  {
+    const long long tpt = kTile / (Hq / Hkv), row_tiles = (T + tpt - 1) / tpt;
+    const long long pt = tiles_of(prefix_cap * page_size) + kItemCost, ot = tiles_of(table_width * page_size) + kItemCost;
+    if ((row_tiles * pt + (row_tiles + B) * ot) * Hkv >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  }
   if (!q || !out || (T > 1 && q_stride < static_cast<long long>(Hq) * D)) return MOE_ERR_INVALID_ARG;
   if (B > 0 && !q_start) return MOE_ERR_INVALID_ARG;
   if (prefix_cap > 0 && (!prefix_pages || !prefix_len)) return MOE_ERR_INVALID_ARG;
@@ -1065,7 +1266,7 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   char* w = static_cast<char*>(ws);
   p.status = reinterpret_cast<int32_t*>(w);
   p.plan = reinterpret_cast<Plan*>(w + L.o_plan);
-  p.first_unit = reinterpret_cast<long long*>(w + L.o_first);
+  p.first_unit = reinterpret_cast<uint32_t*>(w + L.o_first);
   p.ml1 = reinterpret_cast<float2*>(w + L.o_ml1); p.ml2 = reinterpret_cast<float2*>(w + L.o_ml2);
   p.o1 = reinterpret_cast<float*>(w + L.o_o1); p.o2 = reinterpret_cast<float*>(w + L.o_o2);
   // q as [T][key head][group][D], boxes of 64 columns x G heads x tpt tokens;
