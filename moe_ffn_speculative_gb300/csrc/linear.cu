@@ -486,8 +486,8 @@ template <bool kBf16, int kAct>
 cudaError_t launch_many_act(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, int grid,
                             cudaStream_t s) {
   const int smem = 1024 + kManyStages * (kTileBytesA + kManyWide / 2 * 128);
-  cudaError_t e =
-      cudaFuncSetAttribute(linear_many_kernel<kBf16, kAct>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(linear_many_kernel<kBf16, kAct>, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -530,8 +530,8 @@ int cluster_size(int tiles, int k_blocks, int sms) {
 
 template <bool kBf16>
 cudaError_t launch_few(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, cudaStream_t s) {
-  cudaError_t e =
-      cudaFuncSetAttribute(linear_few_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(linear_few_kernel<kBf16>, kLinSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 #ifdef __CUDACC__
 #include <cuda_bf16.h>
@@ -385,6 +387,21 @@ moe_status route_check_args(const uint16_t* x, int T, int H, const uint16_t* gat
 int device_sms();
 bool encode_map_16(CUtensorMap* m, bool f16, const void* base, int rank, const uint64_t* dims,
                    const uint64_t* strides, const uint32_t* box);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `done` is the kernel's own mask of the devices (the first 64) where that has
+// been said, as the call costs a small launch a tenth of its host time.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = d >= 0 && d < 64 ? 1ull << d : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // launchers (route.cu, gemm.cu, combine.cu); return cudaError_t
 cudaError_t launch_route(const RouteParams& p, int tb, cudaStream_t s);

@@ -1187,8 +1187,8 @@ cudaError_t launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, un
 template <bool kBf16, int D>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& p,
                    cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(prefix_attention_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Geometry<D>::kDynamic);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(prefix_attention_kernel<kBf16, D>, Geometry<D>::kDynamic, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;

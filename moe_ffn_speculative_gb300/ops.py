@@ -149,7 +149,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle, without the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -392,37 +393,53 @@ def moe_ffn_forward_mx(x, gate, routed_fmt: int, w_gate_up_q, w_down_q, scales, 
 
 # --------------------------------------------------------------------------- the attention side of the layer
 
+# A small call's time is this file's: each argument is looked at once, and what
+# is wrong with it is worked out only when something is.
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
-def _dtype16(t: torch.Tensor, *others) -> int:
+def _dtype16(t: torch.Tensor) -> int:
     """The library's code of a call's one 16-bit type."""
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("expected a bfloat16 or float16 tensor")
-    for o in others:
-        if o is not None and o.dtype != t.dtype:
-            raise TypeError("the 16-bit tensors of a call have one type")
     return code
 
 
-def _typed(t: Optional[torch.Tensor], dtype, name: str) -> None:
-    if t is not None and t.dtype != dtype:
+def _refuse(t, dtype, name: str) -> None:
+    """Says what keeps `t` from being a contiguous GPU tensor of `dtype`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected a {dtype} tensor")
-
-
-def _heads(t: torch.Tensor, name: str):
-    """(heads, D, row stride) of a [T, heads, D] tensor on the GPU whose rows
-    may lie apart (a slice of a fused projection)."""
     if not t.is_cuda:
-        raise ValueError("tensor is not on a CUDA device")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [T, heads, D]")
-    h, d = t.shape[1], t.shape[2]
-    s = t.stride()
-    if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
-        raise ValueError(f"{name}: the heads of a row are not contiguous")
-    return h, d, (s[0] if t.shape[0] > 1 else h * d)
+        raise ValueError(f"{name}: tensor is not on a CUDA device")
+    raise ValueError(f"{name}: tensor is not contiguous")
+
+
+def _flat(t: Optional[torch.Tensor], dtype, n: int, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, dtype, name)
+    if t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, dtype, T: int, h: int, D: int, name: str) -> int:
+    """Row stride of a [T, h, D] tensor on the GPU whose rows may lie apart (a
+    slice of a fused projection)."""
+    if t.dtype is not dtype or not t.is_cuda:
+        _refuse(t, dtype, name)
+    if t.shape != (T, h, D):
+        raise ValueError(f"{name}: expected [{T}, {h}, {D}]")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and h > 1):
+        if t.numel():
+            raise ValueError(f"{name}: the heads of a row are not contiguous")
+    return s0 if T > 1 else h * D
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, scale: float = 1.0,
@@ -448,56 +465,58 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
     ([pages, page_size, Hkv, D] for a cache of pages), slots int32 [T] their
     rows (negative: not cached; None: row t).  q, k and v may be None.
     -> (q_out, k_cache, v_cache); buffers that are not given are made."""
-    first = q if q is not None else k
-    T = first.shape[0]
-    Hq = Hkv = qs = ks = vs = qos = 0
-    D = first.shape[2]
-    dt = _dtype16(first, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache)
-    _need_cuda(positions, rope, q_weight, k_weight, slots, k_cache, v_cache)
-    _typed(positions, torch.int32, "positions")
-    _typed(slots, torch.int32, "slots")
-    _typed(rope, torch.float32, "rope")
+    lead = q if q is not None else k
+    dt, dtype = _dtype16(lead), lead.dtype
+    if lead.dim() != 3:
+        raise ValueError("expected [T, heads, D]")
+    if k is not None and k.dtype is not dtype:
+        _refuse(k, dtype, "k")
+    T, h, D = lead.shape
+    Hq = Hkv = qs = ks = vs = qos = n_slots = rot = max_pos = 0
+    pk = pv = pkc = pvc = None
     if q is not None:
-        Hq, _, qs = _heads(q, "q")
+        Hq = h
+        qs = _heads(q, dtype, T, h, D, "q")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-        qos = _heads(q_out, "q_out")[2]
-        if q_out.shape != q.shape:
-            raise ValueError("q_out: expected the shape of q")
+            q_out = torch.empty((T, h, D), dtype=dtype, device=q.device)
+            qos = h * D
+        else:
+            qos = _heads(q_out, dtype, T, h, D, "q_out")
     if k is not None:
-        Hkv, dk, ks = _heads(k, "k")
-        if k.shape[0] != T or dk != D:
-            raise ValueError("k: expected the tokens and head size of q")
-        if k_cache is None:
+        if k.dim() != 3:
+            raise ValueError("k: expected [T, heads, D]")
+        Hkv = k.shape[1]
+        ks = _heads(k, dtype, T, Hkv, D, "k")
+        pk = k.data_ptr()
+        if k_cache is None or (v is not None and v_cache is None):
             if slots is not None:
-                raise ValueError("slots name rows of a cache: pass k_cache")
-            k_cache = torch.empty((T, Hkv, D), dtype=k.dtype, device=k.device)
-    n_slots = 0
-    if v is not None:
-        if k is None or v.shape != k.shape:
-            raise ValueError("v: expected the shape of k")
-        vs = _heads(v, "v")[2]
-        if v_cache is None:
-            if slots is not None:
-                raise ValueError("slots name rows of a cache: pass v_cache")
-            v_cache = torch.empty((T, Hkv, D), dtype=v.dtype, device=v.device)
-    elif v_cache is not None:
-        raise ValueError("v_cache without v")
-    for c in (k_cache, v_cache):
-        if c is not None and (Hkv == 0 or c.dim() < 2 or c.shape[-1] != D or c.shape[-2] != Hkv or
-                              c.numel() != k_cache.numel()):
-            raise ValueError("caches: expected [..., Hkv, D] of one size")
-    if k_cache is not None:
-        n_slots = k_cache.numel() // (Hkv * D)
-    rot, max_pos = (0, 0) if rope is None else (rope.shape[1], rope.shape[0])
-    for t, n, name in ((positions, T, "positions"), (slots, T, "slots"), (q_weight, D, "q_weight"),
-                       (k_weight, D, "k_weight")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name}: expected {n} elements")
-    _check(lib().moe_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, Hq, Hkv, D, dt, _ptr(q_weight),
-                                  _ptr(k_weight), eps, _ptr(rope), rot, max_pos, 1 if interleaved else 0,
-                                  _ptr(positions), _ptr(q_out), qos, _ptr(k_cache), _ptr(v_cache), _ptr(slots),
-                                  n_slots, ws.ptr(), ws.nbytes, _stream(stream)), "moe_qk_norm_rope")
+                raise ValueError("slots name rows of a cache: pass k_cache and v_cache")
+            if k_cache is None:
+                k_cache = torch.empty((T, Hkv, D), dtype=dtype, device=k.device)
+            if v is not None and v_cache is None:
+                v_cache = torch.empty((T, Hkv, D), dtype=dtype, device=k.device)
+        size = k_cache.numel()
+        if k_cache.shape[-2:] != (Hkv, D):
+            raise ValueError("k_cache: expected [..., Hkv, D]")
+        n_slots = size // (Hkv * D)
+        pkc = _flat(k_cache, dtype, size, "k_cache")
+        if v is not None:
+            vs = _heads(v, dtype, T, Hkv, D, "v")
+            pv = v.data_ptr()
+            pvc = _flat(v_cache, dtype, size, "v_cache")
+    if (v is not None and k is None) or (v_cache is not None and v is None):
+        raise ValueError("v needs k, v_cache needs v")
+    if rope is not None:
+        max_pos, rot = rope.shape
+        rope = _flat(rope, torch.float32, max_pos * rot, "rope")
+    status = lib().moe_qk_norm_rope(
+        None if q is None else q.data_ptr(), qs, pk, ks, pv, vs, T, Hq, Hkv, D, dt,
+        _flat(q_weight, dtype, D, "q_weight"), _flat(k_weight, dtype, D, "k_weight"), eps, rope, rot, max_pos,
+        1 if interleaved else 0, _flat(positions, torch.int32, T, "positions"),
+        None if q_out is None else q_out.data_ptr(), qos, pkc, pvc, _flat(slots, torch.int32, T, "slots"), n_slots,
+        ws.ptr(), ws.nbytes, _stream(stream))
+    if status:
+        raise MoeError(status, "moe_qk_norm_rope")
     return q_out, k_cache, v_cache
 
 
@@ -518,37 +537,38 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
     both None; page_table int32 [B, width] with own_len int32 [B], or both
     None; scale 1/sqrt(D) unless given; lse fp32 [T,Hq] is written when given.
     -> out [T,Hq,D]."""
-    dt = _dtype16(q, k_cache, v_cache, out)
-    _need_cuda(k_cache, v_cache, q_start, prefix_pages, prefix_len, page_table, own_len, out, lse)
-    Hq, D, qs = _heads(q, "q")
-    T, B = q.shape[0], q_start.numel() - 1
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[3] != D:
-        raise ValueError("caches: expected [pages, page_size, Hkv, D] of one shape")
+    dt, dtype = _dtype16(q), q.dtype
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("expected q [T, Hq, D], caches [pages, page_size, Hkv, D]")
+    T, Hq, D = q.shape
+    qs = _heads(q, dtype, T, Hq, D, "q")
+    pages, page, Hkv, dk = k_cache.shape
+    size = pages * page * Hkv * dk
+    if dk != D:
+        raise ValueError("caches: expected heads of q's size")
+    B = q_start.numel() - 1
     if B < 0 or (prefix_pages is None) != (prefix_len is None) or (page_table is None) != (own_len is None):
         raise ValueError("q_start has B+1 elements; page lists come with their lengths")
-    pages, page, Hkv, _ = k_cache.shape
-    for t, name in ((q_start, "q_start"), (prefix_pages, "prefix_pages"), (prefix_len, "prefix_len"),
-                    (page_table, "page_table"), (own_len, "own_len")):
-        _typed(t, torch.int32, name)
-    _typed(lse, torch.float32, "lse")
-    cap = width = 0
-    if prefix_pages is not None:
-        cap = prefix_pages.numel()
-        if prefix_len.numel() != 1:
-            raise ValueError("prefix_len: expected one element")
+    cap = 0 if prefix_pages is None else prefix_pages.numel()
+    width = 0
     if page_table is not None:
-        if page_table.dim() != 2 or page_table.shape[0] != B or own_len.numel() != B:
-            raise ValueError("page_table: expected [B, width], own_len: [B]")
-        width = page_table.shape[1]
+        rows, width = page_table.shape
+        if rows != B:
+            raise ValueError("page_table: expected [B, width]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
-        raise ValueError("out: expected the shape of q, lse: [T, Hq]")
-    _check(lib().moe_prefix_attention(_ptr(q), qs, T, B, _ptr(q_start), Hq, Hkv, D, dt, _ptr(k_cache), _ptr(v_cache),
-                                      pages, page, _ptr(prefix_pages), cap, _ptr(prefix_len), _ptr(page_table), width,
-                                      _ptr(own_len), 1 if causal else 0, D ** -0.5 if scale is None else scale,
-                                      _ptr(out), _ptr(lse), ws.ptr(), ws.nbytes, _stream(stream)),
-           "moe_prefix_attention")
+        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out: expected the shape of q")
+    i32 = torch.int32
+    status = lib().moe_prefix_attention(
+        q.data_ptr(), qs, T, B, _flat(q_start, i32, B + 1, "q_start"), Hq, Hkv, D, dt,
+        _flat(k_cache, dtype, size, "k_cache"), _flat(v_cache, dtype, size, "v_cache"), pages, page,
+        _flat(prefix_pages, i32, cap, "prefix_pages"), cap, _flat(prefix_len, i32, 1, "prefix_len"),
+        _flat(page_table, i32, B * width, "page_table"), width, _flat(own_len, i32, B, "own_len"), 1 if causal else 0,
+        D ** -0.5 if scale is None else scale, _flat(out, dtype, T * Hq * D, "out"),
+        _flat(lse, torch.float32, T * Hq, "lse"), ws.ptr(), ws.nbytes, _stream(stream))
+    if status:
+        raise MoeError(status, "moe_prefix_attention")
     return out
 
 
@@ -562,43 +582,43 @@ def linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return n
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
-    """Row stride of a matrix on the GPU whose rows may lie apart."""
-    if not t.is_cuda:
-        raise ValueError("tensor is not on a CUDA device")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix")
-    s, n = t.stride(), t.shape[1]
-    if n > 1 and s[1] != 1:
+def _rows(t: torch.Tensor, dtype, m: int, n: int, name: str) -> int:
+    """Row stride of an [m, n] matrix on the GPU whose rows may lie apart."""
+    if t.dtype is not dtype or not t.is_cuda:
+        _refuse(t, dtype, name)
+    if t.shape != (m, n):
+        raise ValueError(f"{name}: expected [{m}, {n}]")
+    s0, s1 = t.stride()
+    if s1 != 1 and n > 1:
         raise ValueError(f"{name}: the elements of a row are not contiguous")
-    return s[0] if t.shape[0] > 1 else n
+    return s0 if m > 1 else n
 
 
 def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=None, y=None, stream=None):
     """act(x w^T + bias) + residual (moe_linear): x [M,K], w [N,K], bias [N],
     residual [M,N]; activation one of ACTIVATIONS; rows of x, residual and y
     may lie apart; residual may be y.  -> y [M,N]."""
-    dt = _dtype16(x, w, bias, residual, y)
-    _need_cuda(w, bias)
-    xs = _rows(x, "x")
+    dt, dtype = _dtype16(x), x.dtype
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("expected x [M, K], w [N, K]")
     M, K = x.shape
     N = w.shape[0]
-    if w.dim() != 2 or w.shape[1] != K or (bias is not None and bias.numel() != N):
-        raise ValueError("w: expected [N, K], bias: [N]")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}")
+    xs = _rows(x, dtype, M, K, "x")
     if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    ys, rs = _rows(y, "y"), 0
+        y = torch.empty((M, N), dtype=dtype, device=x.device)
+        ys = N
+    else:
+        ys = _rows(y, dtype, M, N, "y")
+    rs, pr = 0, None
     if residual is not None:
-        rs = _rows(residual, "residual")
-        if residual.shape != y.shape:
-            raise ValueError("residual: expected [M, N]")
-    if y.shape != (M, N):
-        raise ValueError("y: expected [M, N]")
-    _check(lib().moe_linear(_ptr(x), xs, M, K, _ptr(w), N, dt, _ptr(bias), act, _ptr(residual), rs, _ptr(y), ys,
-                            ws.ptr(), ws.nbytes, _stream(stream)), "moe_linear")
+        rs, pr = _rows(residual, dtype, M, N, "residual"), residual.data_ptr()
+    status = lib().moe_linear(x.data_ptr(), xs, M, K, _flat(w, dtype, N * K, "w"), N, dt, _flat(bias, dtype, N, "bias"),
+                              act, pr, rs, y.data_ptr(), ys, ws.ptr(), ws.nbytes, _stream(stream))
+    if status:
+        raise MoeError(status, "moe_linear")
     return y
 
 
