@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect()) {
       const uint64_t pol = l2_evict_first_policy();
       Ring r;
       int filled = 0;
@@ -156,17 +156,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect()) {
       const uint32_t id = kBf16 ? idesc_bf16(kHalfRows, p.n_tok) : idesc_f16(kHalfRows, p.n_tok);
       Ring r;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = mbar_wait(&c.full[r.stage], r.phase, &c.abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(ring_mem + r.stage * stage_bytes), b = a + kTileBytesA;
+        const uint32_t a = kDescLoK + (smem_u32(ring_mem + r.stage * stage_bytes) >> 4), b = a + kTileBytesA / 16;
 #pragma unroll
         for (int ks = 0; ks < kBlockK / 16; ++ks)
-          mma_bf16(tmem, sw128_desc(a + ks * 32), sw128_desc(b + ks * 32), id, (kb > kb0 || ks > 0) ? 1u : 0u);
+          mma_ss(tmem, a + 2 * ks, kDescHi, b + 2 * ks, kDescHi, id, (kb > kb0 || ks > 0) ? 1u : 0u);
         mma_commit(&c.empty[r.stage]);
         r.next(p.stages);
       }
@@ -273,12 +273,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// mma_ss over both CTAs' halves.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, "
+      "%3};\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrives on the barrier at the same place in both CTAs of the pair when the
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
   if (warp == 0) {
     // this CTA's 128 token rows and its half of the tile's weight rows
-    if (lane == 0) {
+    if (elect()) {
       Ring r;
       int filled = 0;
       bool ok = true;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect()) {
       const uint32_t id = kBf16 ? idesc_bf16(kManyRows, wide) : idesc_f16(kManyRows, wide);
       Ring r;
       bool ok = true;
@@ -419,11 +420,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           ok = mbar_wait(&c.full[r.stage], r.phase, &c.abort_flag);
           if (!ok) { record_failure(p.status, &c.abort_flag, kInfoFull); break; }
           tc_fence_after();
-          const uint32_t a = smem_u32(ring_mem + r.stage * stage_space), b = a + kTileBytesA;
+          const uint32_t a = kDescLoK + (smem_u32(ring_mem + r.stage * stage_space) >> 4), b = a + kTileBytesA / 16;
 #pragma unroll
           for (int ks = 0; ks < kBlockK / 16; ++ks)
-            mma_pair(tmem + buf * kManyWide, sw128_desc(a + ks * 32), sw128_desc(b + ks * 32), id,
-                     (kb > 0 || ks > 0) ? 1u : 0u);
+            mma_pair(tmem + buf * kManyWide, a + 2 * ks, b + 2 * ks, id, (kb > 0 || ks > 0) ? 1u : 0u);
           commit_pair(&c.empty[r.stage]);
           r.next(kManyStages);
         }

@@ -262,18 +262,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A B^T with A from shared or tensor memory (its rows lanes, two
-// 16-bit values a column).  A descriptor's upper word is a constant of its
-// layout and its lower word the address / 16 plus another constant, so that a
-// chain of MMAs costs its issuing thread one addition each.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, "
-      "%4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
+// The same with A from tensor memory: its rows lanes, two 16-bit values a column.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
@@ -282,18 +271,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
       "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // Descriptor of a B operand whose N dimension is contiguous (value rows:
 // 64 columns of one key in 128 bytes, 128-byte swizzle): 8-key groups 1024
 // bytes apart, 64-column blocks kTile * 128 bytes apart.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);       // upper word of either layout
-constexpr uint32_t kDescLoK = 1u << 16;                                    // lower word, K contiguous (as sw128_desc)
-constexpr uint32_t kDescLoN = static_cast<uint32_t>((kTile * 128) >> 4) << 16;  // lower word, N contiguous
+constexpr uint32_t kDescLoN = static_cast<uint32_t>((kTile * 128) >> 4) << 16;  // lower word (kDescHi the upper)
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
