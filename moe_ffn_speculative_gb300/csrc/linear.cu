@@ -31,7 +31,9 @@ namespace moe {
 namespace {
 
 constexpr int kLinThreads = 192;
-constexpr int kLinSmem = 232448 - 1024;  // 227 KB less the control words
+// Half an SM's shared memory: two CTAs are resident, so that a launch's CTAs (and
+// their first weights' way into L2) start while the previous kernel ends.
+constexpr int kLinSmem = 112 * 1024;
 constexpr int kLinMaxStages = 12;
 constexpr int kFewTokens = 128;          // up to this many rows: linear_few_kernel, one tile of tokens
 constexpr int kMaxCluster = 8;
@@ -65,19 +67,25 @@ __device__ __forceinline__ uint16_t from_f(float v) {
   return __half_as_ushort(__float2half_rn(v));
 }
 
-// v sigmoid(v) and the like through one exponential; erfc keeps gelu's
-// negative tail from cancelling.
+// v sigmoid(v) and the like through one exponential (the quotient is 0 where it
+// has run over); erfc keeps gelu's negative tail from cancelling.
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
-    case MOE_ACT_SILU: return v / (1.f + __expf(-v));
+    case MOE_ACT_SILU: return __fdividef(v, 1.f + __expf(-v));
     case MOE_ACT_GELU: return 0.5f * v * erfcf(-v * 0.70710678118654752f);
     case MOE_ACT_GELU_TANH:
-      return v / (1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+      return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
     case MOE_ACT_RELU: return fmaxf(v, 0.f);
     default: return v;
   }
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -128,8 +136,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  griddep_wait();  // what the previous kernel on the stream wrote is visible
   griddep_launch_dependents();
+  // the weights' first tiles come into L2 while the previous kernel ends (what
+  // it writes, weights included, is read only after it)
+  if (warp == 0 && elect())
+    for (int kb = kb0; kb < min(kb1, kb0 + kLinMaxStages); ++kb) tma_prefetch_2d(&tm_w, kb * kBlockK, n0);
+  griddep_wait();  // what the previous kernel on the stream wrote is visible
 
   bool ok = true;
   if (warp == 0) {
@@ -250,7 +262,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // ---------------------------------------------------------------- many rows: CTA pairs
 constexpr int kManyThreads = 320;  // producer, issuer, 8 epilogue warps
 constexpr int kManyEpiWarps = 8;
-constexpr int kManyStages = 6;
+constexpr int kManyStages = 10;    // most stages: as many as fit
+constexpr int kManySmem = 226 * 1024;
 constexpr int kManyRows = 256;     // tokens of a tile, 128 a CTA
 constexpr int kManyWide = 256;     // widest tile, in outputs
 
@@ -313,12 +326,26 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One row's 16 outputs from column n (a multiple of 8 of them below N).
+// One row's outputs [n, n + 32) of those below `end` (both multiples of 8): the
+// residual's loads are under way while the sums come from tensor memory.
 template <bool kBf16, int kAct>
-__device__ __forceinline__ void finish16(const LinearParams& p, const uint32_t (&r)[16], int t, int n) {
+__device__ __forceinline__ void finish32(const LinearParams& p, uint32_t taddr, int t, int n, int end) {
+  uint4 res[4];
+  const bool row = t < p.M;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (n + 8 * h >= p.N) break;
+  for (int h = 0; h < 4; ++h) {
+    res[h] = make_uint4(0, 0, 0, 0);
+    if (p.residual && row && n + 8 * h < end)
+      res[h] = *reinterpret_cast<const uint4*>(p.residual + t * p.res_stride + n + 8 * h);
+  }
+  uint32_t r[32];
+  tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+  tmem_ld16(taddr + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+  tmem_ld_wait();
+  if (!row) return;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if (n + 8 * h >= end) break;
     float v[8], b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * h + i]);
@@ -327,13 +354,12 @@ __device__ __forceinline__ void finish16(const LinearParams& p, const uint32_t (
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += b[i];
     }
+    unpack8<kBf16>(res[h], b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kAct);
-    if (p.residual) {
-      unpack8<kBf16>(*reinterpret_cast<const uint4*>(p.residual + t * p.res_stride + n + 8 * h), b);
+    if (p.residual)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
     *reinterpret_cast<uint4*>(p.y + t * p.y_stride + n + 8 * h) = pack8<kBf16>(v);
   }
 }
@@ -351,11 +377,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const int wide = p.n_tok;  // outputs of a tile
   const int t_tiles = ceil_div(p.M, kManyRows), tiles = t_tiles * ceil_div(p.N, wide);
   const uint32_t stage_bytes = kTileBytesA + static_cast<uint32_t>(wide / 2) * 128;
-  const uint32_t stage_space = kTileBytesA + kManyWide / 2 * 128;
+  // stages start on 1024 bytes: the swizzle's period
+  const uint32_t stage_space = (stage_bytes + 1023u) & ~1023u;
+  const int stages = p.stages;
 
   if (tid == 0) {
     c.abort_flag = 0;
-    for (int s = 0; s < kManyStages; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
+    for (int s = 0; s < stages; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(&c.acc_full[b], 1); mbar_init(&c.acc_empty[b], 2 * kManyEpiWarps); }
     mbar_init(&c.drain, 1);
     fence_barrier_init();
@@ -393,14 +421,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tma_load_2d_pair(a, &tm_x, bar, kb * kBlockK, t0);
           tma_load_2d_pair(a + kTileBytesA, &tm_w, bar, kb * kBlockK, n0);
           ++filled;
-          r.next(kManyStages);
+          r.next(stages);
         }
       }
       if (!ok) record_failure(p.status, &c.abort_flag, kInfoEmpty);
       // both CTAs' copies are counted on the leader's barriers
       if (rank == 0)
-        for (int s = 0; s < kManyStages; ++s) {
-          const int fills = filled / kManyStages + (s < filled % kManyStages ? 1 : 0);
+        for (int s = 0; s < stages; ++s) {
+          const int fills = filled / stages + (s < filled % stages ? 1 : 0);
           if (fills > 0 && !mbar_wait(&c.full[s], (fills - 1) & 1, nullptr))
             record_failure(p.status, &c.abort_flag, kInfoDrain);
         }
@@ -425,7 +453,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           for (int ks = 0; ks < kBlockK / 16; ++ks)
             mma_pair(tmem + buf * kManyWide, a + 2 * ks, b + 2 * ks, id, (kb > 0 || ks > 0) ? 1u : 0u);
           commit_pair(&c.empty[r.stage]);
-          r.next(kManyStages);
+          r.next(stages);
         }
         commit_pair(&c.acc_full[buf]);
       }
@@ -436,25 +464,24 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // rows are lanes; two warps a 32-lane quarter, a half of the columns each
     const int quarter = warp & 3, half = (warp - 2) / 4;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int split = ((wide / 2 + 15) / 16) * 16;
+    const int split = ((wide / 2 + 31) / 32) * 32;
     int i = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++i) {
       const int buf = i & 1;
+      const int t = (tile % t_tiles) * kManyRows + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      const int n0 = (tile / t_tiles) * wide, end = min(n0 + wide, p.N);
+      const int first = n0 + (half ? split : 0), last = half ? end : min(n0 + split, end);
+      if (p.residual && t < p.M)  // into L2 while the products run
+        for (int n = first; n < last; n += 64)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + t * p.res_stride + n));
       const bool got = mbar_wait(&c.acc_full[buf], (i >> 1) & 1, &c.abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
         if (lane == 0) record_failure(p.status, &c.abort_flag, kInfoAccFull);
         break;
       }
       tc_fence_after();
-      const int t = (tile % t_tiles) * kManyRows + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-      const int n0 = (tile / t_tiles) * wide;
-      for (int col = half ? split : 0; col < (half ? wide : split); col += 16) {
-        if (n0 + col >= p.N) break;
-        uint32_t r[16];
-        tmem_ld16(tmem + buf * kManyWide + col + lanes, r);
-        tmem_ld_wait();
-        if (t < p.M) finish16<kBf16, kAct>(p, r, t, n0 + col);
-      }
+      for (int n = first; n < last; n += 32)
+        finish32<kBf16, kAct>(p, tmem + buf * kManyWide + (n - n0) + lanes, t, n, last);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_remote(map_rank(&c.acc_empty[buf], 0));
@@ -485,15 +512,14 @@ int tile_width(int M, int N, int pairs) {
 template <bool kBf16, int kAct>
 cudaError_t launch_many_act(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, int grid,
                             cudaStream_t s) {
-  const int smem = 1024 + kManyStages * (kTileBytesA + kManyWide / 2 * 128);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_many_kernel<kBf16, kAct>, smem, done);
+  cudaError_t e = allow_smem(linear_many_kernel<kBf16, kAct>, kManySmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kManyThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kManySmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -520,11 +546,47 @@ cudaError_t launch_many(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// CTAs that share a weight tile: as many as keep the grid within the SMs and
-// leave each at least 4 of the 64-input k-blocks.
+// How many clusters of c CTAs fit on the current device at once (0 on
+// failure), asked once a device and size: of an empty kernel of the same shape,
+// since the query takes a kernel that allocates tensor memory to fill its SM,
+// whatever it allocates (two CTAs of linear_few_kernel do share one).
+__global__ void __launch_bounds__(kLinThreads, 1) shape_kernel() {}
+
+int resident_clusters(int c) {
+  static std::atomic<int> known[kMaxCluster + 1][64];
+  int d = 0;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return 0;
+  int n = known[c][d].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(shape_kernel, kLinSmem, done) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(c * 1024);  // more than fit
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = kLinSmem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = c;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, shape_kernel, &cfg) != cudaSuccess) return 0;
+  known[c][d].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs that share a weight tile: as many as leave each at least 4 of the
+// 64-input k-blocks, make at most 1.5 CTAs an SM and are resident at once.  (72
+// x 4096 -> 6144, 48 tiles: 26.1, 15.4, 14.0, 12.6, 12.6, 19.4 us with 1 .. 6, of
+// which 6 no longer fit; 9 x 4096 -> 4096, 32 tiles: 16.4, 10.0, 8.7, 7.9, 8.4,
+// 8.1.)
 int cluster_size(int tiles, int k_blocks, int sms) {
   int c = 1;
-  while (c < kMaxCluster && (c + 1) * tiles <= sms && k_blocks / (c + 1) >= 4) ++c;
+  while (c < kMaxCluster && 2 * (c + 1) * tiles <= 3 * sms && k_blocks / (c + 1) >= 4 &&
+         resident_clusters(c + 1) >= tiles)
+    ++c;
   return c;
 }
 
@@ -595,6 +657,8 @@ moe_status moe_linear(const void* x, long long x_stride, int M, int K, const voi
     while (p.tmem_cols < static_cast<uint32_t>(p.n_tok)) p.tmem_cols <<= 1;
   } else {
     p.n_tok = tile_width(M, N, sms / 2);
+    p.stages = (kManySmem - 1024) / ((kTileBytesA + p.n_tok / 2 * 128 + 1023) / 1024 * 1024);
+    if (p.stages > kManyStages) p.stages = kManyStages;
   }
   p.bias = static_cast<const uint16_t*>(bias);
   p.residual = static_cast<const uint16_t*>(residual); p.res_stride = residual_stride;
