@@ -326,23 +326,25 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One row's outputs [n, n + 32) of those below `end` (both multiples of 8): the
-// residual's loads are under way while the sums come from tensor memory.
-template <bool kBf16, int kAct>
-__device__ __forceinline__ void finish32(const LinearParams& p, uint32_t taddr, int t, int n, int end) {
-  uint4 res[4];
-  const bool row = t < p.M;
+// The residual of one row's outputs [n, n + 32), those below `end` (both
+// multiples of 8).
+__device__ __forceinline__ void load_residual(const LinearParams& p, int t, int n, int end, uint4 (&res)[4]) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     res[h] = make_uint4(0, 0, 0, 0);
-    if (p.residual && row && n + 8 * h < end)
+    if (p.residual && t < p.M && n + 8 * h < end)
       res[h] = *reinterpret_cast<const uint4*>(p.residual + t * p.res_stride + n + 8 * h);
   }
+}
+// One row's outputs [n, n + 32) of those below `end`.
+template <bool kBf16, int kAct>
+__device__ __forceinline__ void finish32(const LinearParams& p, uint32_t taddr, int t, int n, int end,
+                                         const uint4 (&res)[4]) {
   uint32_t r[32];
   tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
   tmem_ld16(taddr + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
   tmem_ld_wait();
-  if (!row) return;
+  if (t >= p.M) return;
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     if (n + 8 * h >= end) break;
@@ -354,12 +356,13 @@ __device__ __forceinline__ void finish32(const LinearParams& p, uint32_t taddr, 
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += b[i];
     }
-    unpack8<kBf16>(res[h], b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate(v[i], kAct);
-    if (p.residual)
+    if (p.residual) {
+      unpack8<kBf16>(res[h], b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
     *reinterpret_cast<uint4*>(p.y + t * p.y_stride + n + 8 * h) = pack8<kBf16>(v);
   }
 }
@@ -471,17 +474,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int t = (tile % t_tiles) * kManyRows + static_cast<int>(rank) * 128 + quarter * 32 + lane;
       const int n0 = (tile / t_tiles) * wide, end = min(n0 + wide, p.N);
       const int first = n0 + (half ? split : 0), last = half ? end : min(n0 + split, end);
-      if (p.residual && t < p.M)  // into L2 while the products run
-        for (int n = first; n < last; n += 64)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + t * p.res_stride + n));
+      // the residual, 32 columns ahead of the sums
+      uint4 res[4], next[4];
+      load_residual(p, t, first, last, res);
       const bool got = mbar_wait(&c.acc_full[buf], (i >> 1) & 1, &c.abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
         if (lane == 0) record_failure(p.status, &c.abort_flag, kInfoAccFull);
         break;
       }
       tc_fence_after();
-      for (int n = first; n < last; n += 32)
-        finish32<kBf16, kAct>(p, tmem + buf * kManyWide + (n - n0) + lanes, t, n, last);
+      for (int n = first; n < last; n += 32) {
+        if (n + 32 < last) load_residual(p, t, n + 32, last, next);
+        finish32<kBf16, kAct>(p, tmem + buf * kManyWide + (n - n0) + lanes, t, n, last, res);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) res[h] = next[h];
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_remote(map_rank(&c.acc_empty[buf], 0));
