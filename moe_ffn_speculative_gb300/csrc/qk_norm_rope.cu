@@ -10,11 +10,13 @@
 //
 // The pass reads and writes every row once, so it is bound by memory
 // bandwidth for many tokens and by the latency of its two dependent loads
-// (position, then table row) for few.  A head row is held by D / 8 lanes, 16
-// bytes each, so the norm's sum is a shuffle over those lanes; the pair
-// (i, i + R/2) is another shuffle, the pair (2i, 2i + 1) lies in one lane.  A
-// block takes one token: each lane group walks the token's heads, kHeads rows
-// in flight at a time, and keeps its eight cosines and sines in registers.
+// (position, then table row) for few.  D / 8 lanes hold a head row, each four
+// of its pairs: two runs of four elements R/2 apart (or of neighbours, or, past
+// the rotated part, any two runs).  So a rotation needs no other lane, a lane
+// four cosines and four sines, and the norm's sum one shuffle over those lanes.
+// The norm's weights are multiplied into the cosines and sines once a token, for
+// queries and keys: the row costs 24 multiplications a lane, its factor r last.
+// A block takes one token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -25,8 +27,8 @@
 namespace moe {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kHeads = 4;  // head rows a lane group loads before it uses the first
+constexpr int kRopeThreads = 256;  // most threads of a block
+constexpr int kHeads = 4;          // query rows a lane group loads before it uses the first
 
 struct RopeParams {
   const uint16_t *q, *k, *v;
@@ -66,143 +68,198 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
   return u;
 }
-template <bool kBf16>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A lane's part of a head row: two runs of four elements.
+struct Part {
+  uint2 a, b;
+};
+__device__ __forceinline__ Part load_part(const uint16_t* row, int ea, int eb) {
+  return Part{*reinterpret_cast<const uint2*>(row + ea), *reinterpret_cast<const uint2*>(row + eb)};
+}
+__device__ __forceinline__ void store_part(uint16_t* row, int ea, int eb, const Part& x) {
+  *reinterpret_cast<uint2*>(row + ea) = x.a;
+  *reinterpret_cast<uint2*>(row + eb) = x.b;
+}
+// Its four pairs: element k of both runs, or (kInter) neighbours.
+template <bool kBf16, bool kInter>
+__device__ __forceinline__ void to_pairs(const Part& x, float (&a)[4], float (&b)[4]) {
+  const float2 v[4] = {unpack2<kBf16>(x.a.x), unpack2<kBf16>(x.a.y), unpack2<kBf16>(x.b.x), unpack2<kBf16>(x.b.y)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = unpack2<kBf16>(w[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    if (kInter) {
+      a[i] = v[i].x;
+      b[i] = v[i].y;
+    } else {
+      (i < 2 ? a : b)[2 * (i % 2)] = v[i].x;
+      (i < 2 ? a : b)[2 * (i % 2) + 1] = v[i].y;
+    }
   }
 }
+template <bool kBf16, bool kInter>
+__device__ __forceinline__ Part from_pairs(const float (&a)[4], const float (&b)[4]) {
+  Part x;
+  if (kInter) {
+    x.a = make_uint2(pack2<kBf16>(a[0], b[0]), pack2<kBf16>(a[1], b[1]));
+    x.b = make_uint2(pack2<kBf16>(a[2], b[2]), pack2<kBf16>(a[3], b[3]));
+  } else {
+    x.a = make_uint2(pack2<kBf16>(a[0], a[1]), pack2<kBf16>(a[2], a[3]));
+    x.b = make_uint2(pack2<kBf16>(b[0], b[1]), pack2<kBf16>(b[2], b[3]));
+  }
+  return x;
+}
 
-template <bool kBf16, int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+// The rotation of a lane's pairs with the norm's weights in it:
+// (a, b) -> r (a ca - b sb, b cb + a sa).
+template <bool kBf16, bool kInter, int D>
+struct Turn {
+  float ca[4], sb[4], cb[4], sa[4];
+  bool norm;
+  __device__ __forceinline__ Turn(const float (&c)[4], const float (&s)[4], const uint16_t* weight, int ea, int eb) {
+    norm = weight != nullptr;
+    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+    if (norm) to_pairs<kBf16, kInter>(load_part(weight, ea, eb), wa, wb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ca[i] = wa[i] * c[i];
+      sb[i] = wb[i] * s[i];
+      cb[i] = wb[i] * c[i];
+      sa[i] = wa[i] * s[i];
+    }
+  }
+  // (Every lane of the warp takes part in the sum.)
+  __device__ __forceinline__ Part operator()(const Part& x, float eps) const {
+    float a[4], b[4], ya[4], yb[4], r = 1.f;
+    to_pairs<kBf16, kInter>(x, a, b);
+    if (norm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = rsqrtf(sum * (1.f / D) + eps);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ya[i] = (a[i] * ca[i] - b[i] * sb[i]) * r;
+      yb[i] = (b[i] * cb[i] + a[i] * sa[i]) * r;
+    }
+    return from_pairs<kBf16, kInter>(ya, yb);
+  }
+};
+
+template <bool kBf16, bool kInter, int D>
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;  // lanes of a head row
-  constexpr int kGroups = kRopeThreads / kLanes;
-  const int t = blockIdx.x;
-  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-  const int heads = p.Hq + 2 * p.Hkv;
-
+  const int groups = blockDim.x / kLanes, lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const long long t = blockIdx.x;
   long long slot = t;
   if (p.slots) slot = __ldg(p.slots + t);
   int pos = 0;
   if (p.rot > 0) pos = __ldg(p.positions + t);
-  bool skip = false, cached = slot >= 0;
-  if (pos < 0 || (p.rot > 0 && pos >= p.max_pos)) {
-    skip = true;
-    if (threadIdx.x == 0) record_index(p.status, kInfoPosition);
+
+  // this lane's runs: pairs of the rotated part first, then runs of the rest
+  const int turning = p.rot / 8;  // lanes with rotated pairs
+  int ea, eb;
+  if (kInter || lane >= turning) {
+    ea = kInter ? lane * 8 : p.rot + (lane - turning) * 8;
+    eb = ea + 4;
+  } else {
+    ea = lane * 4;
+    eb = p.rot / 2 + lane * 4;
   }
+  // the first rows' loads are under way while the position is
+  const uint16_t* q = p.q + t * p.q_stride;
+  const uint16_t* k = p.k + t * p.k_stride;
+  const uint16_t* v = p.v + t * p.v_stride;
+  Part xq[kHeads], xk = {}, xv = {};
+#pragma unroll
+  for (int j = 0; j < kHeads; ++j) {
+    xq[j] = Part{};
+    if (group + j * groups < p.Hq) xq[j] = load_part(q + (group + j * groups) * D, ea, eb);
+  }
+  if (group < p.Hkv) {
+    xk = load_part(k + group * D, ea, eb);
+    if (p.v) xv = load_part(v + group * D, ea, eb);
+  }
+
+  bool cached = slot >= 0;
   if (slot >= p.n_slots) {
     cached = false;
     if (threadIdx.x == 0 && p.Hkv > 0) record_index(p.status, kInfoSlot);
   }
-  if (skip) return;
-
-  // this lane's cosines and (signed) sines; 1 and 0 beyond the rotated part
-  const int half = p.rot / 2;
-  const int e0 = lane * 8;
-  float c[8], s[8];
+  if (pos < 0 || (p.rot > 0 && pos >= p.max_pos)) {
+    if (threadIdx.x == 0) record_index(p.status, kInfoPosition);
+    return;
+  }
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (lane < turning) {
+    const float* row = p.rope + static_cast<long long>(pos) * p.rot + lane * 4;
+    const float4 cv = __ldg(reinterpret_cast<const float4*>(row));
+    const float4 sv = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2));
+    c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+    s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+  }
+  {
+    const Turn<kBf16, kInter, D> turn(c, s, p.q_weight, ea, eb);
+    uint16_t* out = p.q_out + t * p.q_out_stride;
+    for (int base = 0; base < p.Hq; base += groups * kHeads) {  // the same count in every lane
+      if (base > 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-  int partner = threadIdx.x & 31;
-  if (e0 < p.rot) {
-    const float* row = p.rope + static_cast<long long>(pos) * p.rot;
-    if (p.interleaved) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + e0 / 2));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + e0 / 2));
-      const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = cc[i];
-        s[2 * i] = -ss[i];
-        s[2 * i + 1] = ss[i];
-      }
-    } else {
-      const bool upper = e0 >= half;
-      const int i0 = upper ? e0 - half : e0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i0 + 4 * j));
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i0 + 4 * j));
-        const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[4 * j + i] = cc[i];
-          s[4 * j + i] = upper ? ss[i] : -ss[i];
+        for (int j = 0; j < kHeads; ++j) {
+          const int h = base + group + j * groups;
+          if (h < p.Hq) xq[j] = load_part(q + h * D, ea, eb);
         }
       }
-      partner += upper ? -(half / 8) : half / 8;
+#pragma unroll
+      for (int j = 0; j < kHeads; ++j) {
+        if (base + j * groups >= p.Hq) break;
+        const int h = base + group + j * groups;
+        const Part y = turn(xq[j], p.eps);
+        if (h < p.Hq) store_part(out + h * D, ea, eb, y);
+      }
     }
   }
-
-  for (int base = 0; base < heads; base += kGroups * kHeads) {  // the same count in every lane
-    const int h0 = base + group;
-    uint4 raw[kHeads];
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j * kGroups;
-      raw[j] = make_uint4(0, 0, 0, 0);
-      const uint16_t* src = nullptr;
-      if (h < p.Hq) src = p.q + t * p.q_stride + h * D;
-      else if (h < p.Hq + p.Hkv) src = p.k + t * p.k_stride + (h - p.Hq) * D;
-      else if (h < heads && p.v) src = p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
-      if (src) raw[j] = *reinterpret_cast<const uint4*>(src + e0);
+  if (p.Hkv == 0) return;
+  const Turn<kBf16, kInter, D> turn(c, s, p.k_weight, ea, eb);
+  for (int base = 0; base < p.Hkv; base += groups) {
+    const int h = base + group;
+    if (base > 0 && h < p.Hkv) {
+      xk = load_part(k + h * D, ea, eb);
+      if (p.v) xv = load_part(v + h * D, ea, eb);
     }
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j * kGroups;
-      // every lane of the warp takes part in the shuffles, whatever its head
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-      float x[8];
-      unpack8<kBf16>(raw[j], x);
-      const uint16_t* weight = is_q ? p.q_weight : p.k_weight;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (weight) {
-        float w[8];
-        unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
-        const float r = rsqrtf(sum * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
-      }
-      float y[8];
-      if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * c[i] + x[i ^ 1] * s[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * c[i] + __shfl_sync(0xffffffffu, x[i], partner) * s[i];
-      }
-      uint4 out;
-      out.x = pack2<kBf16>(y[0], y[1]);
-      out.y = pack2<kBf16>(y[2], y[3]);
-      out.z = pack2<kBf16>(y[4], y[5]);
-      out.w = pack2<kBf16>(y[6], y[7]);
-      if (is_q) {
-        *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D + e0) = out;
-      } else if (h < heads && cached) {
-        if (!is_v)
-          *reinterpret_cast<uint4*>(p.k_cache + (slot * p.Hkv + (h - p.Hq)) * D + e0) = out;
-        else if (p.v)
-          *reinterpret_cast<uint4*>(p.v_cache + (slot * p.Hkv + (h - p.Hq - p.Hkv)) * D + e0) = raw[j];
-      }
+    const Part y = turn(xk, p.eps);
+    if (h < p.Hkv && cached) {
+      const long long row = (slot * p.Hkv + h) * D;
+      store_part(p.k_cache + row, ea, eb, y);
+      if (p.v) store_part(p.v_cache + row, ea, eb, xv);
     }
   }
 }
 
+// Threads of a block: few tokens (a block an SM or fewer) take a lane group for
+// every row, so that no row waits for another; many take eight groups, so that a
+// lane's set-up is spent on several rows.  (16384 tokens of 32 + 2 x 8 heads of
+// 128, with 4, 6, 8, 16 groups: 81, 90, 79, 107 us, and 72 with 64 registers a
+// thread; 1003 of 40 + 2 x 8 heads of 64 with 8, 12, 16, 32: 4.0, 4.0, 4.8, 6.3.)
+template <bool kBf16, bool kInter, int D>
+cudaError_t launch(const RopeParams& p, cudaStream_t s) {
+  int threads = 8 * (D / 8);
+  if (p.T <= device_sms()) {
+    const int rows = p.Hq > p.Hkv ? p.Hq : p.Hkv;
+    threads = (rows * (D / 8) + 31) / 32 * 32;
+    if (threads > kRopeThreads) threads = kRopeThreads;
+  }
+  qk_norm_rope_kernel<kBf16, kInter, D><<<p.T, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+template <bool kBf16, bool kInter>
+cudaError_t launch(const RopeParams& p, int D, cudaStream_t s) {
+  return D == 64    ? launch<kBf16, kInter, 64>(p, s)
+         : D == 128 ? launch<kBf16, kInter, 128>(p, s)
+                    : launch<kBf16, kInter, 256>(p, s);
+}
 template <bool kBf16>
 cudaError_t launch(const RopeParams& p, int D, cudaStream_t s) {
-  switch (D) {
-    case 64: qk_norm_rope_kernel<kBf16, 64><<<p.T, kRopeThreads, 0, s>>>(p); break;
-    case 128: qk_norm_rope_kernel<kBf16, 128><<<p.T, kRopeThreads, 0, s>>>(p); break;
-    default: qk_norm_rope_kernel<kBf16, 256><<<p.T, kRopeThreads, 0, s>>>(p); break;
-  }
-  return cudaGetLastError();
+  return p.interleaved ? launch<kBf16, true>(p, D, s) : launch<kBf16, false>(p, D, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
