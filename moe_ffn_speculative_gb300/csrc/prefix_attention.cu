@@ -393,6 +393,7 @@ struct Producer {
   Ring ring;
   int q_fills[2];   // query tiles loaded so far, per slot
   int kv_fills[2];  // tiles announced so far, per slot
+  bool bad;         // a page outside the cache was seen
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t info) {
     if (mbar_wait(bar, parity, &c.abort_flag)) return true;
@@ -407,14 +408,15 @@ struct Producer {
     ++n;
     return true;
   }
+  // Pages outside the cache become the first one past it: the copy fills zeros.
   __device__ __forceinline__ int page_at(const Segment& s, int i) {
-    const int pg = __ldg(s.pages + i);
-    if (pg >= 0 && pg < p.n_pages) return pg;
-    record_index(p.status, kInfoPage);
-    return p.n_pages;  // out of range: the copy fills zeros
+    const uint32_t pg = static_cast<uint32_t>(__ldg(s.pages + i)), n = static_cast<uint32_t>(p.n_pages);
+    bad |= pg >= n;
+    return static_cast<int>(min(pg, n));
   }
   // The next tile of `slot` (in phase 1, of both: announced to slot 0): a box
-  // for each page and 64-column half.
+  // for each page and 64-column half, four pages' ids read ahead of their
+  // copies where a tile has that many.
   __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment& s, int j, int slot) {
     const int i0 = (j * kTile) >> p.page_log2, boxes = (valid_keys(s, j) + box_rows - 1) / box_rows;
     int pg = page_at(s, i0);
@@ -424,14 +426,29 @@ struct Producer {
     uint8_t* dst = kv_mem + ring.stage * Geo::kTileBytes;
     c.stage_of[slot][entry] = ring.stage;
     mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
-    const int row = (j * kTile) & (p.page - 1);
-    for (int b = 0; b < boxes; ++b) {
-      const int next = b + 1 < boxes ? page_at(s, i0 + b + 1) : 0;
+    const int row = (j * kTile) & (p.page - 1), step = box_rows * 128;
+    int b = 0;
+    for (; b + 4 <= boxes; b += 4) {
+      int ids[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ids[i] = page_at(s, i0 + b + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          tma_load_4d(dst + half * (kTile * 128) + i * step, tm, bar, half * 64, s.h, row, ids[i]);
+      dst += 4 * step;
+    }
+    for (; b < boxes; ++b) {
+      if (b > 0) pg = page_at(s, i0 + b);
 #pragma unroll
       for (int half = 0; half < D / 64; ++half)
         tma_load_4d(dst + half * (kTile * 128), tm, bar, half * 64, s.h, row, pg);
-      dst += box_rows * 128;
-      pg = next;
+      dst += step;
+    }
+    if (bad) {
+      bad = false;
+      record_index(p.status, kInfoPage);
     }
     ++kv_fills[slot];
     ring.next(Geo::kStages);
@@ -693,8 +710,12 @@ struct Softmax {
       const int seen = limit - j * kTile;
       if (__any_sync(0xffffffffu, seen < kTile)) {
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          if (i >= seen) x[i] = 0xff800000u;  // -infinity
+        for (int i = 0; i < kTile; i += 32)
+          if (__any_sync(0xffffffffu, seen < i + 32)) {
+#pragma unroll
+            for (int k = i; k < i + 32; ++k)
+              if (k >= seen) x[k] = 0xff800000u;  // -infinity
+          }
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -745,18 +766,17 @@ struct Softmax {
     o_phase ^= 1u;
     tc_fence_after();
     const long long r = s.part_row + row;
-    float* o = s.phase == 1 ? p.o1 : p.o2;
-#pragma unroll
+    float4* dst = reinterpret_cast<float4*>((s.phase == 1 ? p.o1 : p.o2) + r * D);
+#pragma unroll 1  // what runs once a segment is bound by fetching its code
     for (int i = 0; i < D / 32; ++i) {
       uint32_t y[32];
       tmem_ld32(o_tmem + 32 * i, y);
       tmem_ld_wait();
       if (valid_row) {
-        float4* dst = reinterpret_cast<float4*>(o + r * D + 32 * i);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          dst[k] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]), __uint_as_float(y[4 * k + 2]),
-                               __uint_as_float(y[4 * k + 3]));
+          dst[8 * i + k] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]),
+                                       __uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3]));
       }
     }
     if (valid_row) (s.phase == 1 ? p.ml1 : p.ml2)[r] = make_float2(m, l);
@@ -771,7 +791,7 @@ struct Softmax {
 };
 
 // ---------------------------------------------------------------- planner (warp 3)
-constexpr int kScanAlone = 32;  // up to this many requests one warp scans them, else the whole CTA
+constexpr int kScanAlone = 256;  // up to this many requests one warp scans them, else the whole CTA
 
 // Both slots' places in the phase 2 list: a scan over the requests' units by
 // kThreads threads (a warp, or the CTA).  CTA 0 also leaves it for
@@ -854,34 +874,39 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
   sync();
 }
 
-// Hands a slot's list over, a segment whenever its readers have made room.
-// Lane x is slot x: neither slot waits for the other.
-__device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int slot, int plen) {
+// One slot's list, handed over a segment at a time as its readers make room.
+// (Lane x is slot x: neither slot waits for the other.)
+struct Handing {
   Walker w;
   Segment s;
-  int n = 0;
-  w.begin1(p, plen, blockIdx.x);
+  int n;      // segments handed over
+  bool have;  // s waits to be
+};
+
+// first: only a first segment of phase 1, before the requests are looked at;
+// else the whole list.
+__device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int slot, Handing& g, bool first) {
   long long t0 = clock64();
-  bool have = false;
   while (true) {
-    if (!have) {
-      while (!w.next(p, s)) {
-        if (w.phase == 2) { s.phase = 0; break; }
-        w.begin2(p, 2 * blockIdx.x + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
+    if (!g.have) {
+      while (!g.w.next(p, g.s)) {
+        if (first) return;
+        if (g.w.phase == 2) { g.s.phase = 0; break; }
+        g.w.begin2(p, 2 * blockIdx.x + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
       }
-      if (s.phase == 1 && slot == 1) {  // the pair's second row tile
-        s.tok0 += p.tpt;
-        s.part_row += static_cast<long long>(p.tpt) * p.G;
+      if (g.s.phase == 1 && slot == 1) {  // the pair's second row tile
+        g.s.tok0 += p.tpt;
+        g.s.part_row += static_cast<long long>(p.tpt) * p.G;
       }
-      have = true;
+      g.have = true;
     }
-    const int e = n % kSegments;
-    if (mbar_test_wait(&c.seg_empty[slot][e], ((n / kSegments) & 1) ^ 1u)) {
-      c.seg[slot][e] = s;
+    const int e = g.n % kSegments;
+    if (mbar_test_wait(&c.seg_empty[slot][e], ((g.n / kSegments) & 1) ^ 1u)) {
+      c.seg[slot][e] = g.s;
       mbar_arrive(&c.seg_full[slot][e]);
-      if (s.phase == 0) return;
-      ++n;
-      have = false;
+      ++g.n;
+      g.have = false;
+      if (first || g.s.phase == 0) return;
       t0 = clock64();
     } else {
       if (*static_cast<volatile int*>(&c.abort_flag)) return;
@@ -944,7 +969,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
       if (elect()) {
-        Producer<D> r{p, c, q_mem, kv_mem, &tm_q, &tm_k, &tm_v, min(p.page, kTile), Ring(), {0, 0}, {0, 0}};
+        Producer<D> r{p, c, q_mem, kv_mem, &tm_q, &tm_k, &tm_v, min(p.page, kTile), Ring(), {0, 0}, {0, 0}, false};
         r.run();
         r.drain();
       }
@@ -959,8 +984,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!mbar_wait(&c.drain[slot], 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
       }
     } else if (warp == 3) {
-      if (p.B <= kScanAlone) find_shares<32>(p, c, plen);
-      if (lane < 2) hand_list(p, c, lane, plen);
+      Handing g;
+      g.w.begin1(p, plen, blockIdx.x);
+      g.n = 0;
+      g.have = false;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (lane < 2) hand_list(p, c, lane, g, pass == 0);
+        __syncwarp();
+        if (pass == 0 && p.B <= kScanAlone) find_shares<32>(p, c, plen);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
