@@ -17,13 +17,16 @@
 //   Phase 2: row tiles of one request's block against its own keys, and the
 //     last row tile of the batch against the prefix when their number is odd.
 // Each phase's list of (row tiles, key tile) steps, heads outermost, is cut
-// into equal contiguous shares: one per CTA in phase 1, one per slot in phase
-// 2 (a CTA has two slots, each with its own accumulator), an item counting
-// kItemCost steps more than it has tiles.  So a long context is split over the
-// SMs and short ones are packed.  Every (item, share) leaves its row sums,
-// references and unnormalised fp32 output rows in the workspace, and
-// merge_kernel joins a row's parts in a fixed order: results do not depend on
-// timing.
+// into equal contiguous shares, an item counting kItemCost steps more than it
+// has tiles.  The CTAs are divided between the phases by their work: a CTA of
+// phase 1 takes one share, a CTA of phase 2 two, one for each of its slots (each
+// with its own accumulator).  So a long context is split over the SMs, short
+// ones are packed, and the arithmetic of the one phase runs beside the
+// bandwidth of the other.  (When every CTA took a share of both, there were
+// twice the parts to write and join: the 72-token verify step took 40 us.)
+// Every (item, share) leaves its row sums, references and unnormalised fp32
+// output rows in the workspace, and merge_kernel joins a row's parts in a fixed
+// order: results do not depend on timing.
 //
 // A CTA (one per SM): warp 0 loads query, key and value tiles by TMA (a page
 // is a box of its rows) into a ring of stages; warps 1 and 2 issue the two
@@ -69,9 +72,10 @@ struct AttnParams {
   // workspace
   int32_t* status;
   struct Plan* plan;
-  uint32_t* first_unit;              // [B+1] units of a head's list before each request's
+  struct RequestPlan* requests;      // [B]
+  int32_t* request_of;               // [T] the request of a token, or -1
   float2 *ml1, *ml2;                 // (reference, sum) of every part row, phases 1 and 2
-  float *o1, *o2;                    // their fp32 rows
+  float4 *o1, *o2;                   // their fp32 rows (part_chunk)
 };
 
 // A list of units cut into equal shares: share w holds the units [start(w),
@@ -93,6 +97,20 @@ struct Plan {
   uint32_t per_head;                 // phase 2 units of one head
   int prefix_tiles;
   Shares s1, s2;
+};
+// CTAs of phase 1: a unit of it keeps a CTA busy as long as two of phase 2 (one
+// a slot).
+__device__ __forceinline__ int ctas_of_phase1(uint32_t units1, uint32_t units2, int ctas) {
+  if (units1 == 0) return 0;
+  if (units2 == 0) return ctas;
+  const float u1 = static_cast<float>(units1), u2 = 1.0f * static_cast<float>(units2);
+  const int c = __float2int_rn(static_cast<float>(ctas) * u1 / (u1 + u2));
+  return max(1, min(ctas - 1, c));
+}
+// A request as merge_kernel reads it.
+struct __align__(16) RequestPlan {
+  int a, n, len;         // first token, tokens, own keys
+  uint32_t first_unit;   // units of a head's list before it
 };
 
 // ---------------------------------------------------------------- geometry
@@ -159,25 +177,21 @@ struct Walker {
   Request rq;
   int prefix_len, prefix_tiles;
 
-  // Phase 1, share c of p.ctas.
-  __device__ void begin1(const AttnParams& p, int plen, int c) {
+  // Phase 1, share c.
+  __device__ void begin1(const AttnParams& p, int plen, const Shares& sh, int c) {
     phase = 1; share = c; prefix_len = plen; prefix_tiles = tiles_of(plen);
-    const uint32_t per = units_of(prefix_tiles);
-    const Shares sh = cut(per * p.pairs * p.Hkv, p.ctas);
     const uint32_t u0 = sh.start(c);
     left = sh.start(c + 1) - u0;
-    off = 0; h = i = rt = 0;
-    if (left > 0) {
-      const uint32_t item = u0 / per;
-      off = static_cast<int>(u0 - item * per);
-      h = static_cast<int>(item / p.pairs);
-      i = static_cast<int>(item) - h * p.pairs;
-    }
+    const uint32_t per = units_of(prefix_tiles), item = u0 / per;
+    off = static_cast<int>(u0 - item * per);
+    h = static_cast<int>(item / p.pairs);
+    i = static_cast<int>(item) - h * p.pairs;
+    rt = 0;
   }
-  // Phase 2, share w of 2 * p.ctas; the list position of its first unit was
-  // found by the scan of the requests.
-  __device__ void begin2(const AttnParams& p, int w, uint32_t units, int head, int request, int skip) {
-    phase = 2; share = w;
+  // Phase 2, share w; the list position of its first unit was found by the
+  // scan of the requests.
+  __device__ void begin2(const AttnParams& p, int plen, int w, uint32_t units, int head, int request, int skip) {
+    phase = 2; share = w; prefix_len = plen; prefix_tiles = tiles_of(plen);
     left = units; h = head; i = request; rt = 0; off = skip;
     if (left > 0 && i >= 0) rq = read_request(p, i);
   }
@@ -239,6 +253,14 @@ struct Walker {
     return row * p.G + static_cast<long long>(kTile) * share;
   }
 };
+
+// Part rows lie in blocks of 32, four elements of every row together, so that a
+// warp whose lanes are rows writes 512 bytes at a time: place of elements
+// [4 c, 4 c + 4) of part row r, in float4s.
+template <int D>
+__device__ __forceinline__ long long part_chunk(long long r, int c) {
+  return ((r >> 5) * (D / 4) + c) * 32 + (r & 31);
+}
 
 // ---------------------------------------------------------------- tensor memory, MMA
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -357,7 +379,10 @@ struct Control {
   uint32_t tmem;
   int abort_flag;
   uint32_t sums[kAttnThreads / 32];
-  uint32_t units[2];               // phase 2 shares of the two slots, and where they begin
+  // the CTA's phase and (first) share; of phase 2, each slot's units and place
+  int phase, share;
+  Shares s1;
+  uint32_t units[2];
   int head[2], request[2], skip[2];
 };
 
@@ -766,7 +791,7 @@ struct Softmax {
     o_phase ^= 1u;
     tc_fence_after();
     const long long r = s.part_row + row;
-    float4* dst = reinterpret_cast<float4*>((s.phase == 1 ? p.o1 : p.o2) + r * D);
+    float4* dst = (s.phase == 1 ? p.o1 : p.o2) + part_chunk<D>(r, 0);
 #pragma unroll 1  // what runs once a segment is bound by fetching its code
     for (int i = 0; i < D / 32; ++i) {
       uint32_t y[32];
@@ -775,7 +800,7 @@ struct Softmax {
       if (valid_row) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          dst[8 * i + k] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]),
+          dst[32 * (8 * i + k)] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]),
                                        __uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3]));
       }
     }
@@ -794,8 +819,8 @@ struct Softmax {
 constexpr int kScanAlone = 256;  // up to this many requests one warp scans them, else the whole CTA
 
 // Both slots' places in the phase 2 list: a scan over the requests' units by
-// kThreads threads (a warp, or the CTA).  CTA 0 also leaves it for
-// merge_kernel.
+// kThreads threads (a warp, or the CTA).  What merge_kernel needs of it goes to
+// the workspace.
 template <int kThreads>
 __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int plen) {
   const int lane = threadIdx.x & 31;
@@ -817,29 +842,32 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
     for (int w = 0; w < kWarps; ++w) all += c.sums[w];
     sync();
   }
-  const uint32_t per_head = lead + all;
-  const Shares sh = cut(per_head * p.Hkv, 2 * p.ctas);
-  if (blockIdx.x == 0 && tid == 0) {
-    p.plan->per_head = per_head;
-    p.plan->prefix_tiles = tiles_of(plen);
-    p.plan->s1 = cut(units_of(tiles_of(plen)) * p.pairs * p.Hkv, p.ctas);
-    p.plan->s2 = sh;
-  }
-  // where each slot's share begins in its head's list; below `lead`: inside
-  // the prefix item
+  const uint32_t per_head = lead + all, units1 = units_of(tiles_of(plen)) * p.pairs * p.Hkv;
+  const int c1 = ctas_of_phase1(units1, per_head * p.Hkv, p.ctas);
+  const Shares s1 = cut(units1, max(c1, 1)), s2 = cut(per_head * p.Hkv, max(2 * (p.ctas - c1), 1));
+  if (blockIdx.x == 0 && tid == 0) *p.plan = Plan{per_head, tiles_of(plen), s1, s2};
+  // where each slot's phase 2 share begins in its head's list; below `lead`:
+  // inside the prefix item
+  const int w0 = 2 * (static_cast<int>(blockIdx.x) - c1);
   uint32_t at[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const uint32_t u0 = sh.start(2 * blockIdx.x + x), units = sh.start(2 * blockIdx.x + x + 1) - u0;
+    const uint32_t u0 = w0 >= 0 ? s2.start(w0 + x) : 0, units = w0 >= 0 ? s2.start(w0 + x + 1) - u0 : 0;
     const uint32_t head = units > 0 ? u0 / per_head : 0;
-    at[x] = units > 0 ? u0 - head * per_head : 0;
+    at[x] = units > 0 ? u0 - head * per_head : 0xffffffffu;
     if (tid == 0) {
       c.units[x] = units;
       c.head[x] = static_cast<int>(head);
-      if (units == 0 || at[x] < lead) { c.request[x] = -1; c.skip[x] = static_cast<int>(at[x]); }
+      c.request[x] = -1;
+      c.skip[x] = static_cast<int>(at[x]);
     }
-    if (units == 0) at[x] = 0xffffffffu;
   }
+  if (tid == 0) {
+    c.s1 = s1;
+    c.share = w0 < 0 ? static_cast<int>(blockIdx.x) : w0;
+    c.phase = w0 < 0 ? 1 : 2;
+  }
+  sync();
   uint32_t base = lead;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     uint32_t own = cost0;
@@ -869,44 +897,40 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
         c.request[x] = b;
         c.skip[x] = static_cast<int>(at[x] - first);
       }
-    if (blockIdx.x == 0 && b < p.B) p.first_unit[b] = first;
+    if (b < p.B && b % p.ctas == static_cast<int>(blockIdx.x)) {
+      const Request rq = read_request(p, b);
+      p.requests[b] = RequestPlan{rq.a, rq.n, rq.len, first};
+    }
   }
   sync();
 }
 
-// One slot's list, handed over a segment at a time as its readers make room.
+// Hands a slot's list over, a segment whenever its readers have made room.
 // (Lane x is slot x: neither slot waits for the other.)
-struct Handing {
+__device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int slot, int plen) {
   Walker w;
   Segment s;
-  int n;      // segments handed over
-  bool have;  // s waits to be
-};
-
-// first: only a first segment of phase 1, before the requests are looked at;
-// else the whole list.
-__device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int slot, Handing& g, bool first) {
+  int n = 0;
+  bool have = false;
+  if (c.phase == 1) w.begin1(p, plen, c.s1, c.share);
+  else w.begin2(p, plen, c.share + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
   long long t0 = clock64();
   while (true) {
-    if (!g.have) {
-      while (!g.w.next(p, g.s)) {
-        if (first) return;
-        if (g.w.phase == 2) { g.s.phase = 0; break; }
-        g.w.begin2(p, 2 * blockIdx.x + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
+    if (!have) {
+      if (!w.next(p, s)) s.phase = 0;
+      if (s.phase == 1 && slot == 1) {  // the pair's second row tile
+        s.tok0 += p.tpt;
+        s.part_row += static_cast<long long>(p.tpt) * p.G;
       }
-      if (g.s.phase == 1 && slot == 1) {  // the pair's second row tile
-        g.s.tok0 += p.tpt;
-        g.s.part_row += static_cast<long long>(p.tpt) * p.G;
-      }
-      g.have = true;
+      have = true;
     }
-    const int e = g.n % kSegments;
-    if (mbar_test_wait(&c.seg_empty[slot][e], ((g.n / kSegments) & 1) ^ 1u)) {
-      c.seg[slot][e] = g.s;
+    const int e = n % kSegments;
+    if (mbar_test_wait(&c.seg_empty[slot][e], ((n / kSegments) & 1) ^ 1u)) {
+      c.seg[slot][e] = s;
       mbar_arrive(&c.seg_full[slot][e]);
-      ++g.n;
-      g.have = false;
-      if (first || g.s.phase == 0) return;
+      if (s.phase == 0) return;
+      ++n;
+      have = false;
       t0 = clock64();
     } else {
       if (*static_cast<volatile int*>(&c.abort_flag)) return;
@@ -984,15 +1008,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!mbar_wait(&c.drain[slot], 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
       }
     } else if (warp == 3) {
-      Handing g;
-      g.w.begin1(p, plen, blockIdx.x);
-      g.n = 0;
-      g.have = false;
+      if (p.B <= kScanAlone) find_shares<32>(p, c, plen);
+      if (lane < 2) hand_list(p, c, lane, plen);
+      __syncwarp();
+      // the tokens' requests, for merge_kernel: every CTA writes some
 #pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        if (lane < 2) hand_list(p, c, lane, g, pass == 0);
-        __syncwarp();
-        if (pass == 0 && p.B <= kScanAlone) find_shares<32>(p, c, plen);
+      for (int b = blockIdx.x; b < p.B; b += p.ctas) {
+        const Request rq = read_request(p, b);
+        for (int t = lane; t < rq.n; t += 32) p.request_of[rq.a + t] = b;
       }
     }
   } else {
@@ -1014,48 +1037,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining a row's parts
-// kWarps warps per (token, head).  A row's parts are the shares that hold
-// tiles of its items: consecutive shares.  Their rows are independent loads, so a part costs little more than its bytes; the
-// fewer rows a call has, the more parts each has, and the more warps take it.
+// kWarps warps per token and two of a key head's rows, which lie next to each
+// other in every part: lane l takes row l % 2 and the row's elements from 4 (l /
+// 2), so that it reads whole sectors.  A row's parts are the shares that hold
+// tiles of its items: consecutive shares.  They are independent loads, so a part
+// costs little more than its bytes; the fewer rows a call has, the more parts
+// each has, and the more warps take it.
 struct Parts {
   const float2* ml;
-  const float* o;
+  const float4* o;
   long long row;  // part row of share 0
   int first, count, stride;
   __device__ long long at(int i) const { return row + static_cast<long long>(stride) * (first + i); }
 };
 
+constexpr int merge_threads(int warps) { return warps > 4 ? 32 * warps : 128; }
+
 template <bool kBf16, int D, int kWarps>
-__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kPer = D / 32;
-  __shared__ float2 ml_all[4];
-  __shared__ float acc_all[4][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_warp = warp % kWarps;
-  const long long row = blockIdx.x * (4ll / kWarps) + warp / kWarps;
-  if (row >= static_cast<long long>(p.T) * p.Hq) return;  // whole blocks where kWarps is 4
-  const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row % p.Hq), h = hq / p.G, g = hq % p.G;
+__global__ void __launch_bounds__(merge_threads(kWarps)) merge_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kChunks = D / 64;  // of four elements, a lane
+  constexpr int kUnits = merge_threads(kWarps) / 32 / kWarps;  // of a block
+  __shared__ float2 ml_all[kWarps][2];
+  __shared__ float4 acc_all[kWarps][kChunks][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_warp = warp % kWarps, sub = lane & 1;
+  const int pairs = (p.G + 1) / 2;
+  const long long unit = static_cast<long long>(blockIdx.x) * kUnits + warp / kWarps;
+  if (unit >= static_cast<long long>(p.T) * p.Hkv * pairs) return;  // whole blocks where kWarps > 1
+  const int t = static_cast<int>(unit / (p.Hkv * pairs)), hp = static_cast<int>(unit % (p.Hkv * pairs));
+  const int h = hp / pairs, g = 2 * (hp % pairs);
+  const bool two = g + 1 < p.G;
   griddep_wait();
   const uint32_t per_head = p.plan->per_head;
   const int ptiles = p.plan->prefix_tiles;
   const Shares s1 = p.plan->s1, s2 = p.plan->s2;
-
-  // the request of token t: the last b with q_start[b] <= t, 32 starts a step
-  int lo = 0, n = p.B;
-  while (n > 0) {
-    const int step = (n + 31) / 32;
-    const int i = lo + min(n, (lane + 1) * step) - 1;  // last of this lane's group
-    const bool le = lane * step < n && __ldg(p.q_start + i) <= t;
-    const int groups = __popc(__ballot_sync(0xffffffffu, le));  // whole groups at or before t
-    lo += min(n, groups * step);
-    n = min(step, n - min(n, groups * step));
-    if (step == 1) break;
-    n = n > 0 ? n - 1 : 0;  // the last of the next group is past t
-  }
-  const int b = lo - 1;
-  Request rq;
-  rq.a = rq.n = rq.len = 0;
-  if (b >= 0) rq = read_request(p, b);
-  const bool owned = b >= 0 && t >= rq.a && t < rq.a + rq.n;
+  const int b = p.B > 0 ? p.request_of[t] : -1;
+  RequestPlan rp = {0, 0, 0, 0};
+  // (a token outside every request reads what an earlier call left: checked)
+  if (b >= 0 && b < p.B) rp = p.requests[b];
+  const bool owned = t >= rp.a && t < rp.a + rp.n;
+  const Request rq = {rp.a, rp.n, rp.len};
   Parts run[2];  // the prefix item's parts, the request's
   run[0].count = run[1].count = 0;
   if (owned && ptiles > 0) {
@@ -1075,7 +1095,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Attn
     const int rt = (t - rq.a) / p.tpt;
     const int tiles = tiles_of(rq.seen(p, rt));
     if (tiles > 0) {
-      uint32_t u = h * per_head + p.first_unit[b] + kItemCost;
+      uint32_t u = h * per_head + rp.first_unit + kItemCost;
       for (int i = 0; i < rt; ++i) u += units_of(tiles_of(rq.seen(p, i)));
       Parts& r = run[1];
       r.ml = p.ml2; r.o = p.o2; r.stride = kTile;
@@ -1084,67 +1104,90 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Attn
       r.row = Walker::part_row(p, 2, h, t, true, 0) + g;
     }
   }
-  float m = -INFINITY, l = 0.f, acc[kPer];
+  // of both rows: reference and sum; of this lane's: its elements
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float4 acc[kChunks];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i0 = 0; i0 < run[k].count; i0 += 32 * kWarps) {
+  for (int i = 0; i < kChunks; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const Parts r = run[k];
+#pragma unroll 1
+    for (int i0 = 0; i0 < r.count; i0 += 32 * kWarps) {
       // lane i: this warp's i-th part of the chunk
       const int i = i0 + lane * kWarps + part_warp;
-      const long long at = i < run[k].count ? run[k].at(i) : -1;
-      const float2 ml = at >= 0 ? run[k].ml[at] : make_float2(-INFINITY, 0.f);
-      float top = ml.x;
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1;
-      const float old = ex2(m - base), mine = ex2(ml.x - base);
-      m = m1;
-      float sum = mine * ml.y;
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      l = l * old + sum;
+      const long long at = i < r.count ? r.at(i) : -1;
+      float mine[2], old[2];
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) acc[x] *= old;
-      const int count = min(32, (run[k].count - i0 - part_warp + kWarps - 1) / kWarps);
+      for (int x = 0; x < 2; ++x) {
+        const float2 ml = at >= 0 && (x == 0 || two) ? r.ml[at + x] : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m1 = fmaxf(m[x], top), base = m1 == -INFINITY ? 0.f : m1;
+        old[x] = ex2(m[x] - base);
+        mine[x] = ex2(ml.x - base);
+        m[x] = m1;
+        float sum = mine[x] * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[x] = l[x] * old[x] + sum;
+      }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const float f = sub ? old[1] : old[0];
+        acc[c].x *= f; acc[c].y *= f; acc[c].z *= f; acc[c].w *= f;
+      }
+      const int count = min(32, (r.count - i0 - part_warp + kWarps - 1) / kWarps);
 #pragma unroll 8
       for (int x = 0; x < count; ++x) {
-        const long long r = __shfl_sync(0xffffffffu, at, x);
-        const float a = __shfl_sync(0xffffffffu, mine, x);
-        if (r >= 0) {
-          const float* src = run[k].o + r * D + lane * kPer;
-          if (kPer == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-            acc[0] += a * v.x; acc[1] += a * v.y; acc[kPer - 2] += a * v.z; acc[kPer - 1] += a * v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            acc[0] += a * v.x; acc[1] += a * v.y;
-          }
+        const long long row = __shfl_sync(0xffffffffu, at, x) + (two ? sub : 0);
+        const float a0 = __shfl_sync(0xffffffffu, mine[0], x), a1 = __shfl_sync(0xffffffffu, mine[1], x);
+        const float a = sub ? a1 : a0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const float4 v = __ldcg(r.o + part_chunk<D>(row, lane / 2 + 16 * c));
+          acc[c].x += a * v.x; acc[c].y += a * v.y; acc[c].z += a * v.z; acc[c].w += a * v.w;
         }
       }
     }
+  }
   if (kWarps > 1) {
-    if (lane == 0) ml_all[warp] = make_float2(m, l);
+    if (lane < 2) ml_all[warp][lane] = make_float2(m[lane], l[lane]);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc_all[warp][lane * kPer + i] = acc[i];
+    for (int c = 0; c < kChunks; ++c) acc_all[warp][c][lane] = acc[c];
     __syncthreads();
     if (warp != 0) return;
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml_all[w].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    l = 0.f;
+    float top = -INFINITY, sum = 0.f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_all[w][sub].x);
+    const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    for (int c = 0; c < kChunks; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = 0; w < kWarps; ++w) {
-      const float a = ex2(ml_all[w].x - base);
-      l += a * ml_all[w].y;
+      const float a = ex2(ml_all[w][sub].x - base);
+      sum += a * ml_all[w][sub].y;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += a * acc_all[w][lane * kPer + i];
+      for (int c = 0; c < kChunks; ++c) {
+        const float4 v = acc_all[w][c][lane];
+        acc[c].x += a * v.x; acc[c].y += a * v.y; acc[c].z += a * v.z; acc[c].w += a * v.w;
+      }
     }
+    m[0] = m[1] = top;
+    l[0] = l[1] = sum;
   }
-  const float base = m == -INFINITY ? 0.f : m;
-  const float r = l > 0.f ? 1.f / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kPer);
+  if (sub && !two) return;
+  const float top = sub ? m[1] : m[0], sum = sub ? l[1] : l[0];
+  const float base = top == -INFINITY ? 0.f : top;
+  const float f = sum > 0.f ? 1.f / sum : 0.f;
+  const long long row = static_cast<long long>(t) * p.Hq + h * p.G + g + sub;
 #pragma unroll
-  for (int i = 0; i < kPer / 2; ++i) dst[i] = l == 0.f ? 0u : pack2<kBf16>(acc[2 * i] * r, acc[2 * i + 1] * r);
-  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+  for (int c = 0; c < kChunks; ++c) {
+    const float4 v = acc[c];
+    const uint2 out = sum == 0.f ? make_uint2(0u, 0u)
+                                 : make_uint2(pack2<kBf16>(v.x * f, v.y * f), pack2<kBf16>(v.z * f, v.w * f));
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * (lane / 2 + 16 * c)) = out;
+  }
+  if (lane < 2 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1158,11 +1201,11 @@ moe_status shape_status(int T, int B, int Hq, int Hkv, int D) {
   return MOE_OK;
 }
 
-// Workspace after the fixed header: the plan, the requests' first units, the
+// Workspace after the fixed header: the plan, the requests, the tokens' requests, the
 // parts' (reference, sum) pairs and rows.
 struct AttnLayout {
   int tpt, pairs, left;
-  size_t o_plan, o_first, o_ml1, o_ml2, o_o1, o_o2, total;
+  size_t o_plan, o_req, o_of, o_ml1, o_ml2, o_o1, o_o2, total;
 };
 AttnLayout attn_layout(int T, int B, int Hq, int Hkv, int D, int ctas) {
   AttnLayout L;
@@ -1175,11 +1218,12 @@ AttnLayout attn_layout(int T, int B, int Hq, int Hkv, int D, int ctas) {
   const size_t rows2 = (static_cast<size_t>(T) + l0) * Hq + 2ull * kTile * ctas;
   size_t o = kWsHeaderBytes;
   L.o_plan = o; o += kWsAlign;
-  L.o_first = o; o += ws_align_up(4 * (static_cast<size_t>(B) + 1));
+  L.o_req = o; o += ws_align_up(sizeof(RequestPlan) * static_cast<size_t>(B));
+  L.o_of = o; o += ws_align_up(4 * static_cast<size_t>(T));
   L.o_ml1 = o; o += ws_align_up(8 * rows1);
   L.o_ml2 = o; o += ws_align_up(8 * rows2);
-  L.o_o1 = o; o += ws_align_up(4 * rows1 * D);
-  L.o_o2 = o; o += ws_align_up(4 * rows2 * D);
+  L.o_o1 = o; o += ws_align_up(4 * ((rows1 + 31) / 32 * 32) * D);
+  L.o_o2 = o; o += ws_align_up(4 * ((rows2 + 31) / 32 * 32) * D);
   L.total = o;
   return L;
 }
@@ -1209,12 +1253,18 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUten
   launch_config(&cfg, &attr, static_cast<unsigned>(p.ctas), kAttnThreads, Geometry<D>::kDynamic, s);
   e = cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kBf16, D>, tm_q, tm_k, tm_v, p);
   if (e != cudaSuccess) return e;
-  // four warps a row while the rows leave the SMs room for them
-  const long long rows = static_cast<long long>(p.T) * p.Hq;
-  const bool wide = rows <= 32ll * p.ctas;
-  launch_config(&cfg, &attr, static_cast<unsigned>(wide ? rows : (rows + 3) / 4), 128, 0, s);
-  return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 4>, p)
-              : cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 1>, p);
+  // warps a unit of two rows: more while the units leave the SMs room for them
+  const long long units = static_cast<long long>(p.T) * p.Hkv * ((p.G + 1) / 2);
+  if (units <= 4ll * p.ctas) {
+    launch_config(&cfg, &attr, static_cast<unsigned>(units), merge_threads(8), 0, s);
+    return cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 8>, p);
+  }
+  if (units <= 16ll * p.ctas) {
+    launch_config(&cfg, &attr, static_cast<unsigned>(units), merge_threads(4), 0, s);
+    return cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 4>, p);
+  }
+  launch_config(&cfg, &attr, static_cast<unsigned>((units + 3) / 4), merge_threads(1), 0, s);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<kBf16, D, 1>, p);
 }
 
 }  // namespace
@@ -1280,9 +1330,10 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   char* w = static_cast<char*>(ws);
   p.status = reinterpret_cast<int32_t*>(w);
   p.plan = reinterpret_cast<Plan*>(w + L.o_plan);
-  p.first_unit = reinterpret_cast<uint32_t*>(w + L.o_first);
+  p.requests = reinterpret_cast<RequestPlan*>(w + L.o_req);
+  p.request_of = reinterpret_cast<int32_t*>(w + L.o_of);
   p.ml1 = reinterpret_cast<float2*>(w + L.o_ml1); p.ml2 = reinterpret_cast<float2*>(w + L.o_ml2);
-  p.o1 = reinterpret_cast<float*>(w + L.o_o1); p.o2 = reinterpret_cast<float*>(w + L.o_o2);
+  p.o1 = reinterpret_cast<float4*>(w + L.o_o1); p.o2 = reinterpret_cast<float4*>(w + L.o_o2);
   // q as [T][key head][group][D], boxes of 64 columns x G heads x tpt tokens;
   // the caches as [page][slot][key head][D], boxes of 64 columns x one head x
   // up to 128 slots (without any page nothing is loaded: q stands in)
