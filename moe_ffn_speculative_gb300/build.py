@@ -1,11 +1,13 @@
 """Builds libmoe_gb300.so in-tree with nvcc for sm_103a (one translation unit
-per .cu file, compiled in parallel, linked with the static CUDA runtime)."""
+per .cu file, compiled in parallel, linked with the static CUDA runtime), and
+_binding.so, the attention side's calls for this interpreter and its torch."""
 from __future__ import annotations
 
 import os
 import platform
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", platform.machine())
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["route.cu", "gemm.cu", "slice.cu", "mx.cu", "api.cu", "noalloc.cu", "qk_norm_rope.cu",
            "prefix_attention.cu", "linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -56,8 +59,10 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {cmd[-3]}")
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_binding_object, run)
         list(ex.map(run, jobs))
+        binding_obj, binding_key, linked_with = binding.result()
     stamp = os.path.join(BUILD, "lib.stamp")
     if jobs or _stale(LIB, objs) or not os.path.exists(stamp):
         tmp = LIB + ".tmp"
@@ -65,7 +70,47 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         os.replace(tmp, LIB)
         with open(stamp, "w") as f:
             f.write(platform.machine())
+    _link(BINDING, binding_obj, binding_key, linked_with, run)
     return LIB
+
+
+def _same(path: str, text: str) -> bool:
+    if not os.path.exists(path):
+        return False
+    with open(path) as f:
+        return f.read() == text
+
+
+def _binding_object(run):
+    """Compiles csrc/binding.cpp; -> (object, what it was compiled for, the
+    linker's arguments)."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    lib, inc_torch = os.path.join(at, "lib"), os.path.join(at, "include")
+    key = f"{platform.machine()} {torch.__version__} {sys.version}"
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    stamp = os.path.join(BUILD, "binding.compiled")
+    if _stale(obj, [src, os.path.join(INCLUDE, "moe.h")]) or not _same(stamp, key):
+        inc = [a for p in (inc_torch, os.path.join(inc_torch, "torch", "csrc", "api", "include"),
+                           sysconfig.get_paths()["include"], INCLUDE, cuda) for a in ("-I", p)]
+        run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *inc,
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c", src, "-o", obj])
+        with open(stamp, "w") as f:
+            f.write(key)
+    return obj, key, ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
+
+
+def _link(target: str, obj: str, key: str, args, run) -> None:
+    stamp = os.path.join(BUILD, "binding.stamp")
+    if not _stale(target, [obj]) and _same(stamp, key):
+        return
+    tmp = target + ".tmp"
+    run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L", PKG, "-l:libmoe_gb300.so", *args,
+         "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, target)
+    with open(stamp, "w") as f:
+        f.write(key)
 
 
 if __name__ == "__main__":

@@ -7,6 +7,7 @@ when the library is missing or the device is not a CUDA GPU the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 from typing import Optional, Tuple
@@ -392,9 +393,29 @@ def moe_ffn_forward_mx(x, gate, routed_fmt: int, w_gate_up_q, w_down_q, scales, 
 
 
 # --------------------------------------------------------------------------- the attention side of the layer
+#
+# A small call's time is the binding's.  These calls go through _binding.so
+# (csrc/binding.cpp), which checks every argument and calls the library; it
+# answers None where one of them is not as it has to be, and the checks below,
+# which then run, say which and why.
 
-# A small call's time is this file's: each argument is looked at once, and what
-# is wrong with it is worked out only when something is.
+_binding_module = None
+
+
+def _binding():
+    """The extension module; raises if it has not been built."""
+    global _binding_module
+    if _binding_module is None:
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with moe_ffn_speculative_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding_module = module
+    return _binding_module
+
+
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
@@ -466,6 +487,15 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
     rows (negative: not cached; None: row t).  q, k and v may be None.
     -> (q_out, k_cache, v_cache); buffers that are not given are made."""
     lead = q if q is not None else k
+    if lead.is_cuda and (k is None) == (k_cache is None) and (v is None) == (v_cache is None):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        status = _binding().qk_norm_rope(q, k, v, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_cache,
+                                         v_cache, slots, ws.ptr(), ws.nbytes, _stream(stream))
+        if status == 0:
+            return q_out, k_cache, v_cache
+        if status is not None:
+            raise MoeError(status, "moe_qk_norm_rope")
     dt, dtype = _dtype16(lead), lead.dtype
     if lead.dim() != 3:
         raise ValueError("expected [T, heads, D]")
@@ -537,6 +567,18 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
     both None; page_table int32 [B, width] with own_len int32 [B], or both
     None; scale 1/sqrt(D) unless given; lse fp32 [T,Hq] is written when given.
     -> out [T,Hq,D]."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if not q.is_cuda:
+        _refuse(q, q.dtype, "q")
+    status = _binding().prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, page_table, own_len,
+                                         causal, scale, out, lse, ws.ptr(), ws.nbytes, _stream(stream))
+    if status == 0:
+        return out
+    if status is not None:
+        raise MoeError(status, "moe_prefix_attention")
     dt, dtype = _dtype16(q), q.dtype
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("expected q [T, Hq, D], caches [pages, page_size, Hkv, D]")
@@ -555,9 +597,7 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
         rows, width = page_table.shape
         if rows != B:
             raise ValueError("page_table: expected [B, width]")
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
-    elif out.shape != q.shape:
+    if out.shape != q.shape:
         raise ValueError("out: expected the shape of q")
     i32 = torch.int32
     status = lib().moe_prefix_attention(
@@ -565,7 +605,7 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
         _flat(k_cache, dtype, size, "k_cache"), _flat(v_cache, dtype, size, "v_cache"), pages, page,
         _flat(prefix_pages, i32, cap, "prefix_pages"), cap, _flat(prefix_len, i32, 1, "prefix_len"),
         _flat(page_table, i32, B * width, "page_table"), width, _flat(own_len, i32, B, "own_len"), 1 if causal else 0,
-        D ** -0.5 if scale is None else scale, _flat(out, dtype, T * Hq * D, "out"),
+        scale, _flat(out, dtype, T * Hq * D, "out"),
         _flat(lse, torch.float32, T * Hq, "lse"), ws.ptr(), ws.nbytes, _stream(stream))
     if status:
         raise MoeError(status, "moe_prefix_attention")
@@ -598,14 +638,23 @@ def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=No
     """act(x w^T + bias) + residual (moe_linear): x [M,K], w [N,K], bias [N],
     residual [M,N]; activation one of ACTIVATIONS; rows of x, residual and y
     may lie apart; residual may be y.  -> y [M,N]."""
-    dt, dtype = _dtype16(x), x.dtype
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("expected x [M, K], w [N, K]")
-    M, K = x.shape
-    N = w.shape[0]
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("expected x [M, K], w [N, K]")
+    if y is None:
+        y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+    if not x.is_cuda:
+        _refuse(x, x.dtype, "x")
+    status = _binding().linear(x, w, bias, act, residual, y, ws.ptr(), ws.nbytes, _stream(stream))
+    if status == 0:
+        return y
+    if status is not None:
+        raise MoeError(status, "moe_linear")
+    dt, dtype = _dtype16(x), x.dtype
+    M, K = x.shape
+    N = w.shape[0]
     xs = _rows(x, dtype, M, K, "x")
     if y is None:
         y = torch.empty((M, N), dtype=dtype, device=x.device)
