@@ -816,32 +816,25 @@ struct Softmax {
 };
 
 // ---------------------------------------------------------------- planner (warp 3)
-constexpr int kScanAlone = 256;  // up to this many requests one warp scans them, else the whole CTA
-
 // Both slots' places in the phase 2 list: a scan over the requests' units by
-// kThreads threads (a warp, or the CTA).  What merge_kernel needs of it goes to
-// the workspace.
-template <int kThreads>
+// the whole CTA (a warp alone takes longer even over 8 requests).  What
+// merge_kernel needs of it goes to the workspace.
 __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int plen) {
-  const int lane = threadIdx.x & 31;
-  const int tid = kThreads == 32 ? lane : threadIdx.x, warp = kThreads == 32 ? 0 : threadIdx.x >> 5;
-  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kAttnThreads / 32;
   const uint32_t lead = p.left ? units_of(tiles_of(plen)) : 0;  // the prefix item comes first
-  const auto sync = [] { if (kThreads == 32) __syncwarp(); else __syncthreads(); };
   uint32_t mine = 0, cost0 = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
+  for (int b = tid; b < p.B; b += kAttnThreads) {
     const uint32_t u = read_request(p, b).units(p);
     if (b == tid) cost0 = u;
     mine += u;
   }
   uint32_t all = __reduce_add_sync(0xffffffffu, mine);
-  if (kThreads != 32) {
-    if (lane == 0) c.sums[warp] = all;
-    sync();
-    all = 0;
-    for (int w = 0; w < kWarps; ++w) all += c.sums[w];
-    sync();
-  }
+  if (lane == 0) c.sums[warp] = all;
+  __syncthreads();
+  all = 0;
+  for (int w = 0; w < kWarps; ++w) all += c.sums[w];
+  __syncthreads();
   const uint32_t per_head = lead + all, units1 = units_of(tiles_of(plen)) * p.pairs * p.Hkv;
   const int c1 = ctas_of_phase1(units1, per_head * p.Hkv, p.ctas);
   const Shares s1 = cut(units1, max(c1, 1)), s2 = cut(per_head * p.Hkv, max(2 * (p.ctas - c1), 1));
@@ -867,11 +860,11 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
     c.share = w0 < 0 ? static_cast<int>(blockIdx.x) : w0;
     c.phase = w0 < 0 ? 1 : 2;
   }
-  sync();
   uint32_t base = lead;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
+    const int b = b0 + tid;
     uint32_t own = cost0;
-    if (b0 > 0) own = b0 + tid < p.B ? read_request(p, b0 + tid).units(p) : 0;
+    if (b0 > 0) own = b < p.B ? read_request(p, b).units(p) : 0;
     uint32_t inc = own;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -879,18 +872,13 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
       if (lane >= o) inc += v;
     }
     uint32_t first = base + inc - own;
-    if (kThreads == 32) {
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    } else {
-      if (lane == 31) c.sums[warp] = inc;
-      sync();
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) first += c.sums[w];
-        base += c.sums[w];
-      }
-      sync();
+    if (lane == 31) c.sums[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) first += c.sums[w];
+      base += c.sums[w];
     }
-    const int b = b0 + tid;
+    __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
       if (at[x] >= first && at[x] - first < own) {
@@ -902,7 +890,6 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
       p.requests[b] = RequestPlan{rq.a, rq.n, rq.len, first};
     }
   }
-  sync();
 }
 
 // Hands a slot's list over, a segment whenever its readers have made room.
@@ -981,9 +968,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   }
+  // merge_kernel's blocks may be placed as this grid's leave (they wait for all
+  // of it)
+  griddep_launch_dependents();
   griddep_wait();  // what the previous kernel on the stream wrote is visible
   const int plen = p.prefix_cap > 0 ? held(__ldg(p.prefix_len), p.prefix_cap, p.page, p.status) : 0;
-  if (p.B > kScanAlone) find_shares<kAttnThreads>(p, c, plen);
+  find_shares(p, c, plen);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1008,7 +998,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!mbar_wait(&c.drain[slot], 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoAttnDrain);
       }
     } else if (warp == 3) {
-      if (p.B <= kScanAlone) find_shares<32>(p, c, plen);
       if (lane < 2) hand_list(p, c, lane, plen);
       __syncwarp();
       // the tokens' requests, for merge_kernel: every CTA writes some
@@ -1026,7 +1015,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tmem + 2 * kTile + slot * kTile + lanes, 0, 0};
     r.run();
   }
-  griddep_launch_dependents();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
