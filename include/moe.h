@@ -21,6 +21,10 @@
  *      ungated (DeepSeek), added to the weighted combine of the routed
  *      experts (PR #48763 commit note on DraftMoE forward).
  *
+ * Around the layer, at the end of this file: the attention side of the same
+ * decoder layer (q/k norms with rotation and cache write, attention over a
+ * shared prefix and own pages, projections with their epilogue).
+ *
  * Conventions (every entry point):
  *   - Every tensor pointer is a DEVICE pointer owned by the caller; tensors are
  *     contiguous, row-major.  bf16 tensors are passed as raw 16-bit words.
@@ -529,7 +533,9 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
  * Limits: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 128, Hq <= 1024;
  * page_size a power of two from 8 to 1024; T <= MOE_MAX_ATTN_TOKENS, B <=
  * MOE_MAX_REQUESTS, prefix_cap and table_width times page_size <=
- * MOE_MAX_KEYS; 0 < scale < infinity; pointers 16-byte aligned. */
+ * MOE_MAX_KEYS, the work of a call below 2^31 (key head, tile of tokens, tile
+ * of 128 keys) steps; 0 < scale < infinity; q_stride >= Hq D; pointers 16-byte
+ * aligned. */
 #define MOE_MAX_REQUESTS 65536
 #define MOE_MAX_KEYS 268435456
 MOE_API size_t moe_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
