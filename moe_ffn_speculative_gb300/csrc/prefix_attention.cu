@@ -11,7 +11,9 @@
 // rarely rescaled and no power exceeds 2^8 (the ratio is exact whatever m is).
 //
 // Work.  The G = Hq / Hkv heads of a token that read one key head are rows of
-// one product, so a row tile is floor(128 / G) tokens x G heads.
+// one product, so a row tile is floor(128 / G) tokens x G heads (in phase 2
+// floor(64 / G) where the blocks are that short: the query tiles then leave
+// room for another stage of keys, and half of the MMA's rows are idle).
 //   Phase 1: the prefix against pairs of row tiles of the whole batch: each key
 //     tile is loaded once for 256 rows.
 //   Phase 2: row tiles of one request's block against its own keys, and the
@@ -60,7 +62,9 @@ constexpr int kAttnSmem = 232448;    // 227 KB
 constexpr int kRegsFew = 104, kRegsMany = 200;
 
 struct AttnParams {
-  int T, B, Hq, Hkv, G, tpt;         // tpt: tokens of a row tile
+  int T, B, Hq, Hkv, G;
+  int tpt, tpt2;                     // tokens of a row tile of phase 1, of phase 2
+  int compact;                       // 1: phase 2's row tiles have at most 64 rows
   int n_pages, page, page_log2;
   const int32_t *q_start, *prefix_pages, *prefix_len, *page_table, *own_len;
   int prefix_cap, table_width, causal;
@@ -98,12 +102,16 @@ struct Plan {
   int prefix_tiles;
   Shares s1, s2;
 };
-// CTAs of phase 1: a unit of it keeps a CTA busy as long as two of phase 2 (one
-// a slot).
-__device__ __forceinline__ int ctas_of_phase1(uint32_t units1, uint32_t units2, int ctas) {
+// CTAs of phase 1.  A unit of it keeps a CTA busy for about 2500 clocks, one of
+// phase 2 (two slots at a time) for 0.75 as long and 0.028 more for every box
+// that a tile is copied in.  (64 requests over 16384 shared keys, pages of 64,
+// with a factor of 0.6, 0.8, 1: 182, 151, 170 us; draft blocks over 30011, pages
+// of 16: 87, 80, 77.)
+__device__ __forceinline__ int ctas_of_phase1(uint32_t units1, uint32_t units2, int ctas, int page) {
   if (units1 == 0) return 0;
   if (units2 == 0) return ctas;
-  const float u1 = static_cast<float>(units1), u2 = 1.0f * static_cast<float>(units2);
+  const float cost = 0.75f + 0.028f * static_cast<float>(page < kTile ? kTile / page : 1);
+  const float u1 = static_cast<float>(units1), u2 = cost * static_cast<float>(units2);
   const int c = __float2int_rn(static_cast<float>(ctas) * u1 / (u1 + u2));
   return max(1, min(ctas - 1, c));
 }
@@ -129,10 +137,10 @@ struct Request {
   // keys seen by the last token of row tile rt
   __device__ int seen(const AttnParams& p, int rt) const {
     if (!p.causal) return len;
-    const int last = min(n, (rt + 1) * p.tpt);
+    const int last = min(n, (rt + 1) * p.tpt2);
     return max(0, min(len, len - n + last));
   }
-  __device__ int row_tiles(const AttnParams& p) const { return (n + p.tpt - 1) / p.tpt; }
+  __device__ int row_tiles(const AttnParams& p) const { return (n + p.tpt2 - 1) / p.tpt2; }
   __device__ uint32_t units(const AttnParams& p) const {
     uint32_t u = 0;
     const int k = row_tiles(p);
@@ -224,7 +232,7 @@ struct Walker {
           s.keys = prefix_len; s.own = 0; s.lim0 = 0;
           s.pages = p.prefix_pages;
         } else {
-          s.tok0 = rq.a + rt * p.tpt;
+          s.tok0 = rq.a + rt * p.tpt2;
           s.tok_end = rq.a + rq.n;
           s.keys = rq.seen(p, rt); s.own = p.causal; s.lim0 = rq.len - rq.n - rq.a + 1;
           s.pages = p.page_table + static_cast<long long>(i) * p.table_width;
@@ -353,8 +361,21 @@ struct Geometry {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQBufs = D == 64 ? 2 : 1;  // query tiles a slot
   // 2 KB for the control words, 1 KB to align the tiles
-  static constexpr int kStages = (kAttnSmem - 2048 - 1024 - 2 * kQBufs * kTileBytes) / kTileBytes;
-  static constexpr int kDynamic = 1024 + (2 * kQBufs + kStages) * kTileBytes;
+  static constexpr int kSpace = (kAttnSmem - 2048 - 1024) / kTileBytes * kTileBytes;
+  static constexpr int kDynamic = 1024 + kSpace;
+};
+// Shared memory of a CTA: the query tiles (whole, or 64 rows each), then as many
+// stages of keys and values as fit.
+template <int D>
+struct Room {
+  int q_bytes, q_half;  // of a query tile, and of its 64-column half
+  int stages;
+  __device__ explicit Room(bool compact) {
+    using Geo = Geometry<D>;
+    q_bytes = compact ? Geo::kTileBytes / 2 : Geo::kTileBytes;
+    q_half = q_bytes / (D / 64);
+    stages = (Geo::kSpace - 2 * Geo::kQBufs * q_bytes) / Geo::kTileBytes;
+  }
 };
 
 // Key and value tiles land in a ring of stages in the order that the producer
@@ -406,6 +427,10 @@ __device__ __forceinline__ bool take(Control& c, int slot, int& n, Segment& s, i
 __device__ __forceinline__ int valid_keys(const Segment& s, int j) { return min(kTile, s.keys - j * kTile); }
 
 // ---------------------------------------------------------------- TMA producer (one thread of warp 0)
+// One copy of the load serves both slots, keys and values: a slot's state is
+// selected, not unrolled, since this thread is bound by fetching its code (with
+// six inlined copies a load took it 1300 clocks, and the own keys' bandwidth
+// was that).
 template <int D>
 struct Producer {
   using Geo = Geometry<D>;
@@ -414,127 +439,143 @@ struct Producer {
   uint8_t* q_mem;
   uint8_t* kv_mem;
   const CUtensorMap *tm_q, *tm_k, *tm_v;
+  Room<D> room;
   int box_rows;     // rows of a box: a page's, up to a tile's
+  int q_tokens;     // tokens of a query tile
   Ring ring;
-  int q_fills[2];   // query tiles loaded so far, per slot
-  int kv_fills[2];  // tiles announced so far, per slot
-  bool bad;         // a page outside the cache was seen
+  int q_fills0, q_fills1;    // query tiles loaded so far, per slot
+  int kv_fills0, kv_fills1;  // tiles announced so far, per slot
+  bool bad;                  // a page outside the cache was seen
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t info) {
     if (mbar_wait(bar, parity, &c.abort_flag)) return true;
     record_failure(p.status, &c.abort_flag, info);
     return false;
   }
-  __device__ __forceinline__ bool take(int slot, int& n, Segment& s) {
-    const int e = n % kSegments;
-    if (!wait(&c.seg_full[slot][e], (n / kSegments) & 1, kInfoAttnList)) return false;
-    s = c.seg[slot][e];
-    mbar_arrive(&c.seg_empty[slot][e]);
-    ++n;
-    return true;
+  // The slot's n-th segment, read where it lies until it is released.
+  __device__ __forceinline__ const Segment* take(int slot, int n) {
+    if (!wait(&c.seg_full[slot][n % kSegments], (n / kSegments) & 1, kInfoAttnList)) return nullptr;
+    return &c.seg[slot][n % kSegments];
   }
+  __device__ __forceinline__ void release(int slot, int n) { mbar_arrive(&c.seg_empty[slot][n % kSegments]); }
   // Pages outside the cache become the first one past it: the copy fills zeros.
-  __device__ __forceinline__ int page_at(const Segment& s, int i) {
-    const uint32_t pg = static_cast<uint32_t>(__ldg(s.pages + i)), n = static_cast<uint32_t>(p.n_pages);
+  __device__ __forceinline__ int page_at(const int32_t* pages, int i) {
+    const uint32_t pg = static_cast<uint32_t>(__ldg(pages + i)), n = static_cast<uint32_t>(p.n_pages);
     bad |= pg >= n;
     return static_cast<int>(min(pg, n));
   }
+  __device__ __forceinline__ int boxes(int keys, int j) const {
+    return (min(kTile, keys - j * kTile) + box_rows - 1) / box_rows;
+  }
+  // The first two pages of tile j.
+  __device__ __forceinline__ void first_pages(const Segment* s, int j, int& a, int& b) {
+    const int32_t* pages = s->pages + ((j * kTile) >> p.page_log2);
+    a = page_at(pages, 0);
+    b = boxes(s->keys, j) > 1 ? page_at(pages, 1) : 0;
+  }
   // The next tile of `slot` (in phase 1, of both: announced to slot 0): a box
-  // for each page and 64-column half, four pages' ids read ahead of their
-  // copies where a tile has that many.
-  __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment& s, int j, int slot) {
-    const int i0 = (j * kTile) >> p.page_log2, boxes = (valid_keys(s, j) + box_rows - 1) / box_rows;
-    int pg = page_at(s, i0);
+  // for each page and 64-column half.
+  __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment* s, int j, int slot, int a, int b) {
     if (!wait(&c.kv_empty[ring.stage], ring.phase ^ 1u, kInfoAttnStage)) return false;
-    const int entry = kv_fills[slot] % kSequence;
+    const int n = boxes(s->keys, j), h = s->h, fills = slot ? kv_fills1++ : kv_fills0++, entry = fills % kSequence;
     uint64_t* bar = &c.kv_full[slot][entry];
     uint8_t* dst = kv_mem + ring.stage * Geo::kTileBytes;
     c.stage_of[slot][entry] = ring.stage;
-    mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
+    mbar_arrive_expect_tx(bar, n * box_rows * D * 2);
     const int row = (j * kTile) & (p.page - 1), step = box_rows * 128;
-    int b = 0;
-    for (; b + 4 <= boxes; b += 4) {
-      int ids[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ids[i] = page_at(s, i0 + b + i);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half)
-          tma_load_4d(dst + half * (kTile * 128) + i * step, tm, bar, half * 64, s.h, row, ids[i]);
-      dst += 4 * step;
-    }
-    for (; b < boxes; ++b) {
-      if (b > 0) pg = page_at(s, i0 + b);
+    const int32_t* pages = s->pages + ((j * kTile) >> p.page_log2);
+#pragma unroll 1
+    for (int i = 0; i < n; i += 2) {
+      const int a1 = i + 2 < n ? page_at(pages, i + 2) : 0, b1 = i + 3 < n ? page_at(pages, i + 3) : 0;
 #pragma unroll
       for (int half = 0; half < D / 64; ++half)
-        tma_load_4d(dst + half * (kTile * 128), tm, bar, half * 64, s.h, row, pg);
-      dst += step;
+        tma_load_4d(dst + half * (kTile * 128), tm, bar, half * 64, h, row, a);
+      if (i + 1 < n) {
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          tma_load_4d(dst + half * (kTile * 128) + step, tm, bar, half * 64, h, row, b);
+      }
+      dst += 2 * step;
+      a = a1;
+      b = b1;
     }
-    if (bad) {
-      bad = false;
-      record_index(p.status, kInfoPage);
-    }
-    ++kv_fills[slot];
-    ring.next(Geo::kStages);
+    ring.next(room.stages);
     return true;
   }
-  __device__ __forceinline__ bool load_q(const Segment& s, int slot) {
-    const int n = q_fills[slot]++, buf = n % Geo::kQBufs;
+  __device__ __forceinline__ bool load_q(const Segment* s, int slot) {
+    const int n = slot ? q_fills1++ : q_fills0++, buf = n % Geo::kQBufs;
     if (!wait(&c.q_empty[slot][buf], ((n / Geo::kQBufs) & 1) ^ 1u, kInfoAttnQuery)) return false;
     uint64_t* bar = &c.q_full[slot][buf];
-    uint8_t* dst = q_mem + (slot * Geo::kQBufs + buf) * Geo::kTileBytes;
-    mbar_arrive_expect_tx(bar, p.G * p.tpt * D * 2);
+    uint8_t* dst = q_mem + (slot * Geo::kQBufs + buf) * room.q_bytes;
+    mbar_arrive_expect_tx(bar, p.G * q_tokens * D * 2);
 #pragma unroll
     for (int half = 0; half < D / 64; ++half)
-      tma_load_4d(dst + half * (kTile * 128), tm_q, bar, half * 64, 0, s.h, s.tok0);
+      tma_load_4d(dst + half * room.q_half, tm_q, bar, half * 64, 0, s->h, s->tok0);
     return true;
   }
 
-  __device__ __forceinline__ bool run() {
-    Segment u[2];
-    int n[2] = {0, 0}, j[2] = {0, 0};
-    if (!take(0, n[0], u[0]) || !take(1, n[1], u[1])) return false;
-    // phase 1: the slots' segments differ in their row tile only
-    while (u[0].phase == 1) {
-      if (!load_q(u[0], 0) || !load_q(u[1], 1)) return false;
-      for (int i = u[0].j0; i < u[0].j1; ++i)
-        if (!load_kv(tm_k, u[0], i, 0) || !load_kv(tm_v, u[0], i, 0)) return false;
-      if (!take(0, n[0], u[0]) || !take(1, n[1], u[1])) return false;
-    }
-    // phase 2: each slot its own; a slot's next keys follow its values
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (u[x].phase) {
-        j[x] = u[x].j0;
-        if (!load_q(u[x], x) || !load_kv(tm_k, u[x], j[x], x)) return false;
-      }
-    while (u[0].phase || u[1].phase) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!u[x].phase) continue;
-        if (!load_kv(tm_v, u[x], j[x], x)) return false;
-        if (++j[x] == u[x].j1) {
-          if (!take(x, n[x], u[x])) return false;
-          if (!u[x].phase) continue;
-          j[x] = u[x].j0;
-          if (!load_q(u[x], x)) return false;
+  // In turn, each slot's values of tile j and keys of tile j + 1 (the first
+  // time, only the keys of its first).  In phase 1 slot 0's tiles serve both,
+  // whose segments differ in their row tile only.
+  __device__ __forceinline__ bool run(bool phase2) {
+    int n0 = 0, n1 = 0, j0 = -1, j1 = -1;      // segment and tile of each slot (-1: none yet)
+    int a0 = 0, b0 = 0, a1 = 0, b1 = 0;        // the tile's first pages
+    bool live0 = true, live1 = phase2;
+#pragma unroll 1
+    for (int x = 0; live0 || live1; x = phase2 ? x ^ 1 : 0) {
+      if (!(x ? live1 : live0)) continue;
+      int n = x ? n1 : n0, j = x ? j1 : j0, pa = x ? a1 : a0, pb = x ? b1 : b0;
+      const Segment* s = &c.seg[x][n % kSegments];
+      bool fresh = j < 0;
+      int na = 0, nb = 0;  // the next tile's pages, under way during this one's values
+      if (!fresh) {
+        const bool more = j + 1 < s->j1;
+        if (more) first_pages(s, j + 1, na, nb);
+        if (!load_kv(tm_v, s, j, x, pa, pb)) return false;
+        ++j;
+        if (!more) {
+          release(x, n);
+          if (!phase2) release(1, n);
+          ++n;
+          fresh = true;
         }
-        if (!load_kv(tm_k, u[x], j[x], x)) return false;
       }
+      bool ended = false;
+      if (fresh) {
+        if ((s = take(x, n)) == nullptr) return false;
+        const Segment* other = s;
+        if (!phase2 && (other = take(1, n)) == nullptr) return false;
+        ended = s->phase == 0;
+        if (!ended) {
+          j = s->j0;
+          first_pages(s, j, na, nb);
+          if (!load_q(s, x) || (!phase2 && !load_q(other, 1))) return false;
+        }
+      }
+      if (!ended && !load_kv(tm_k, s, j, x, na, nb)) return false;
+      if (bad) {
+        bad = false;
+        record_index(p.status, kInfoPage);
+      }
+      if (x) { n1 = n; j1 = j; a1 = na; b1 = nb; live1 = !ended; }
+      else { n0 = n; j0 = j; a0 = na; b0 = nb; live0 = !ended; }
     }
     return true;
   }
   // Every copy that was issued has landed (also after a failure).
   __device__ void drain() {
     bool ok = true;
+#pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
+      const int kv = slot ? kv_fills1 : kv_fills0, q = slot ? q_fills1 : q_fills0;
+#pragma unroll 1
       for (int e = 0; e < kSequence; ++e) {
-        const int fills = kv_fills[slot] / kSequence + (e < kv_fills[slot] % kSequence ? 1 : 0);
+        const int fills = kv / kSequence + (e < kv % kSequence ? 1 : 0);
         if (fills > 0) ok &= mbar_wait(&c.kv_full[slot][e], (fills - 1) & 1, nullptr);
       }
+#pragma unroll 1
       for (int b = 0; b < Geo::kQBufs; ++b) {
-        const int fills = q_fills[slot] / Geo::kQBufs + (b < q_fills[slot] % Geo::kQBufs ? 1 : 0);
+        const int fills = q / Geo::kQBufs + (b < q % Geo::kQBufs ? 1 : 0);
         if (fills > 0) ok &= mbar_wait(&c.q_full[slot][b], (fills - 1) & 1, nullptr);
       }
     }
@@ -554,6 +595,7 @@ struct Issuer {
   const AttnParams& p;
   Control& c;
   uint32_t q_lo, kv_lo;  // lower descriptor words of the slot's first query tile and of stage 0
+  uint32_t q_tile, q_half;  // from one query tile to the next, from one half of it to the other
   uint32_t s_tmem;       // the slot's S (and P); O lies 2 tiles further
   int slot;
   int q_uses, seen;      // query tiles and key/value tiles taken so far
@@ -621,12 +663,12 @@ struct Issuer {
   // slot's follow them without a gap.
   __device__ __forceinline__ void scores(const Keys& k) {
     const uint32_t id = idesc(((k.valid + 15) / 16) * 16);
-    const uint32_t a = kDescLoK + q_lo + k.q_buf * (Geo::kTileBytes / 16);
+    const uint32_t a = kDescLoK + q_lo + k.q_buf * q_tile;
     const uint32_t b = kDescLoK + kv_lo + k.stage * (Geo::kTileBytes / 16);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      const uint32_t o = (ks / 4) * (kTile * 128 / 16) + (ks % 4) * 2;
-      mma_ss(s_tmem, a + o, kDescHi, b + o, kDescHi, id, ks > 0 ? 1u : 0u);
+      mma_ss(s_tmem, a + (ks / 4) * q_half + (ks % 4) * 2, kDescHi,
+             b + (ks / 4) * (kTile * 128 / 16) + (ks % 4) * 2, kDescHi, id, ks > 0 ? 1u : 0u);
       if (ks == D / 16 - 4 && !alone) mbar_arrive(&c.turn[slot ^ 1]);
     }
     mma_commit(&c.s_full[slot]);
@@ -715,7 +757,7 @@ struct Softmax {
   }
   __device__ __forceinline__ bool segment(const Segment& s) {
     const int tok = s.tok0 + row / p.G;
-    const bool valid_row = row < p.tpt * p.G && tok < s.tok_end;
+    const bool valid_row = row < (s.phase == 1 ? p.tpt : p.tpt2) * p.G && tok < s.tok_end;
     const int limit = s.own ? max(0, min(s.keys, s.lim0 + tok)) : s.keys;
     // a warp without a valid row (a block of few tokens) only keeps step
     const bool idle = !__any_sync(0xffffffffu, valid_row);
@@ -836,7 +878,7 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
   for (int w = 0; w < kWarps; ++w) all += c.sums[w];
   __syncthreads();
   const uint32_t per_head = lead + all, units1 = units_of(tiles_of(plen)) * p.pairs * p.Hkv;
-  const int c1 = ctas_of_phase1(units1, per_head * p.Hkv, p.ctas);
+  const int c1 = ctas_of_phase1(units1, per_head * p.Hkv, p.ctas, p.page);
   const Shares s1 = cut(units1, max(c1, 1)), s2 = cut(per_head * p.Hkv, max(2 * (p.ctas - c1), 1));
   if (blockIdx.x == 0 && tid == 0) *p.plan = Plan{per_head, tiles_of(plen), s1, s2};
   // where each slot's phase 2 share begins in its head's list; below `lead`:
@@ -932,13 +974,13 @@ __device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int s
 
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    prefix_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnParams p) {
+    prefix_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q2,
+                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ AttnParams p) {
   using Geo = Geometry<D>;
   extern __shared__ uint8_t dynamic[];
   __shared__ Control c;
   uint8_t* q_mem = dynamic + ((1024u - (smem_u32(dynamic) & 1023u)) & 1023u);
-  uint8_t* kv_mem = q_mem + 2 * Geo::kQBufs * Geo::kTileBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -956,11 +998,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&c.seg_empty[s / kSegments][s % kSegments], kReaders);
     }
     for (int s = 0; s < kSequence; ++s) { mbar_init(&c.kv_full[0][s], 1); mbar_init(&c.kv_full[1][s], 1); }
-    for (int s = 0; s < Geo::kStages; ++s) mbar_init(&c.kv_empty[s], 2);
+    for (int s = 0; s < kSequence; ++s) mbar_init(&c.kv_empty[s], 2);
     mbar_init(&c.drain[0], 1);
     mbar_init(&c.drain[1], 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_q2);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
@@ -978,18 +1021,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
+  const bool phase2 = c.phase == 2;
+  const Room<D> room(phase2 && p.compact);
+  uint8_t* kv_mem = q_mem + 2 * Geo::kQBufs * room.q_bytes;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
       if (elect()) {
-        Producer<D> r{p, c, q_mem, kv_mem, &tm_q, &tm_k, &tm_v, min(p.page, kTile), Ring(), {0, 0}, {0, 0}, false};
-        r.run();
+        Producer<D> r{p,    c,    q_mem, kv_mem, phase2 ? &tm_q2 : &tm_q, &tm_k, &tm_v, room, min(p.page, kTile),
+                      phase2 ? p.tpt2 : p.tpt, Ring(), 0, 0, 0, 0, false};
+        r.run(phase2);
         r.drain();
       }
     } else if (warp <= 2) {
       const int slot = warp - 1;
-      Issuer<kBf16, D> r{p, c, smem_u32(q_mem + slot * Geo::kQBufs * Geo::kTileBytes) >> 4, smem_u32(kv_mem) >> 4,
+      Issuer<kBf16, D> r{p, c, smem_u32(q_mem + slot * Geo::kQBufs * room.q_bytes) >> 4, smem_u32(kv_mem) >> 4,
+                         static_cast<uint32_t>(room.q_bytes) >> 4, static_cast<uint32_t>(room.q_half) >> 4,
                          tmem + slot * kTile, slot, 0, 0, 0, 0u, slot == 0, false};
       r.run(kv_mem);
       // every MMA issued above has completed once `drain` flips
@@ -1080,7 +1128,7 @@ __global__ void __launch_bounds__(merge_threads(kWarps)) merge_kernel(const __gr
     r.row = Walker::part_row(p, paired ? 1 : 2, h, t, false, 0) + g;
   }
   if (owned) {
-    const int rt = (t - rq.a) / p.tpt;
+    const int rt = (t - rq.a) / p.tpt2;
     const int tiles = tiles_of(rq.seen(p, rt));
     if (tiles > 0) {
       uint32_t u = h * per_head + rp.first_unit + kItemCost;
@@ -1192,15 +1240,24 @@ moe_status shape_status(int T, int B, int Hq, int Hkv, int D) {
 // Workspace after the fixed header: the plan, the requests, the tokens' requests, the
 // parts' (reference, sum) pairs and rows.
 struct AttnLayout {
-  int tpt, pairs, left;
+  int tpt, tpt2, compact, pairs, left;
   size_t o_plan, o_req, o_of, o_ml1, o_ml2, o_o1, o_o2, total;
 };
 AttnLayout attn_layout(int T, int B, int Hq, int Hkv, int D, int ctas) {
   AttnLayout L;
-  L.tpt = kTile / (Hq / Hkv);
+  const int G = Hq / Hkv;
+  L.tpt = kTile / G;
+  // phase 2 in tiles of 64 rows where the requests' blocks have that many on
+  // average: longer ones would read their keys twice as often
+  L.compact = G <= kTile / 2 && static_cast<long long>(T) * G <= kTile / 2 * static_cast<long long>(B) ? 1 : 0;
+  L.tpt2 = L.compact ? kTile / 2 / G : L.tpt;
   const int row_tiles = ceil_div(T, L.tpt);
   L.pairs = row_tiles / 2;
   L.left = row_tiles % 2;
+  if (L.left && T - 2 * L.pairs * L.tpt > L.tpt2) {  // too long for phase 2: a pair with an empty second tile
+    ++L.pairs;
+    L.left = 0;
+  }
   const int l0 = L.left ? T - 2 * L.pairs * L.tpt : 0;
   const size_t rows1 = L.pairs ? static_cast<size_t>(T) * Hq + 2ull * kTile * ctas : 0;
   const size_t rows2 = (static_cast<size_t>(T) + l0) * Hq + 2ull * kTile * ctas;
@@ -1231,15 +1288,15 @@ cudaError_t launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, un
 }
 
 template <bool kBf16, int D>
-cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& p,
-                   cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_q2, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                   const AttnParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(prefix_attention_kernel<kBf16, D>, Geometry<D>::kDynamic, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   launch_config(&cfg, &attr, static_cast<unsigned>(p.ctas), kAttnThreads, Geometry<D>::kDynamic, s);
-  e = cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kBf16, D>, tm_q, tm_k, tm_v, p);
+  e = cudaLaunchKernelEx(&cfg, prefix_attention_kernel<kBf16, D>, tm_q, tm_q2, tm_k, tm_v, p);
   if (e != cudaSuccess) return e;
   // warps a unit of two rows: more while the units leave the SMs room for them
   const long long units = static_cast<long long>(p.T) * p.Hkv * ((p.G + 1) / 2);
@@ -1286,7 +1343,7 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   if (T == 0) return MOE_OK;
   // units of both phases' lists, at most, in 31 bits
   {
-    const long long tpt = kTile / (Hq / Hkv), row_tiles = (T + tpt - 1) / tpt;
+    const long long tpt = kTile / (Hq / Hkv), row_tiles = 2 * ((T + tpt - 1) / tpt) + 2;
     const long long pt = tiles_of(prefix_cap * page_size) + kItemCost, ot = tiles_of(table_width * page_size) + kItemCost;
     if ((row_tiles * pt + (row_tiles + B) * ot) * Hkv >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
   }
@@ -1306,7 +1363,8 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   AttnParams p;
   memset(&p, 0, sizeof(p));
-  p.T = T; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.tpt = L.tpt;
+  p.T = T; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.tpt = L.tpt; p.tpt2 = L.tpt2; p.compact = L.compact;
   p.n_pages = n_pages; p.page = page_size;
   while ((1 << p.page_log2) < page_size) ++p.page_log2;
   p.q_start = q_start; p.prefix_pages = prefix_pages; p.prefix_len = prefix_len; p.page_table = page_table;
@@ -1326,23 +1384,25 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   // the caches as [page][slot][key head][D], boxes of 64 columns x one head x
   // up to 128 slots (without any page nothing is loaded: q stands in)
   const bool f16 = dtype == MOE_DTYPE_F16;
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q, tm_q2, tm_k, tm_v;
   const uint64_t hd = static_cast<uint64_t>(D);
   const uint64_t qd[4] = {hd, static_cast<uint64_t>(p.G), static_cast<uint64_t>(Hkv), static_cast<uint64_t>(T)};
   const uint64_t qs[3] = {hd * 2, hd * 2 * p.G, static_cast<uint64_t>(T > 1 ? q_stride : Hq * D) * 2};
   const uint32_t qb[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt)};
+  const uint32_t qb2[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt2)};
   const bool pages = prefix_cap + table_width > 0;
   const uint64_t kd[4] = {hd, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(page_size),
                           static_cast<uint64_t>(pages ? n_pages : 1)};
   const uint64_t ks[3] = {hd * 2, hd * 2 * Hkv, hd * 2 * Hkv * page_size};
   const uint32_t kb[4] = {64, 1, static_cast<uint32_t>(page_size < kTile ? page_size : kTile), 1};
-  if (!encode_map_16(&tm_q, f16, q, 4, qd, qs, qb) || !encode_map_16(&tm_k, f16, pages ? k_cache : q, 4, kd, ks, kb) ||
+  if (!encode_map_16(&tm_q, f16, q, 4, qd, qs, qb) || !encode_map_16(&tm_q2, f16, q, 4, qd, qs, qb2) ||
+      !encode_map_16(&tm_k, f16, pages ? k_cache : q, 4, kd, ks, kb) ||
       !encode_map_16(&tm_v, f16, pages ? v_cache : q, 4, kd, ks, kb))
     return MOE_ERR_CUDA;
-  const cudaError_t e = f16 ? (D == 64 ? launch<false, 64>(tm_q, tm_k, tm_v, p, stream)
-                                       : launch<false, 128>(tm_q, tm_k, tm_v, p, stream))
-                            : (D == 64 ? launch<true, 64>(tm_q, tm_k, tm_v, p, stream)
-                                       : launch<true, 128>(tm_q, tm_k, tm_v, p, stream));
+  const cudaError_t e = f16 ? (D == 64 ? launch<false, 64>(tm_q, tm_q2, tm_k, tm_v, p, stream)
+                                       : launch<false, 128>(tm_q, tm_q2, tm_k, tm_v, p, stream))
+                            : (D == 64 ? launch<true, 64>(tm_q, tm_q2, tm_k, tm_v, p, stream)
+                                       : launch<true, 128>(tm_q, tm_q2, tm_k, tm_v, p, stream));
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
