@@ -354,3 +354,66 @@ def test_indexes_outside_their_tables():
     b.q_start[0] = 0
     assert torch.equal(b.run(True)[0], want)
     assert b.ws.device_status() == (ops.MOE_OK, 0)
+
+
+@pytest.mark.gpu
+def test_no_requests_and_no_pages():
+    """A batch without requests, without a prefix or without own pages."""
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+    q = torch.randn((5, 4, 64), device="cuda").to(BF)
+    k = torch.randn((3, 8, 2, 64), device="cuda").to(BF)
+    ws = ops.Workspace(ops.prefix_attention_workspace_bytes(5, 2, 4, 2, 64))
+    lse = torch.zeros((5, 4), device="cuda")
+    out = ops.prefix_attention(q, k, k, i32(0), i32(1), i32(8), None, None, ws, lse=lse)  # B = 0: all padding
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    out = ops.prefix_attention(q, k, k, i32(0, 2, 5), None, None, None, None, ws, lse=lse)
+    assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+    only_prefix = ops.prefix_attention(q, k, k, i32(0, 2, 5), i32(1, 2), i32(11), None, None, ws)
+    keys = k[1:3].flatten(0, 1)[:11].double().repeat_interleave(2, 1)
+    z = torch.einsum("nhd,mhd->hnm", q.double(), keys) * 64 ** -0.5
+    want = torch.einsum("hnm,mhd->nhd", z.softmax(-1), keys)
+    assert (only_prefix.double() - want).norm() <= 0.5 * torch.finfo(BF).eps * want.norm()
+    assert ws.device_status() == (ops.MOE_OK, 0)
+    empty = ops.prefix_attention(q[:0], k, k, i32(0, 0, 0), i32(1), i32(8), None, None, ws)
+    assert empty.shape == (0, 4, 64)
+
+
+@pytest.mark.gpu
+def test_pages_past_32_bit_offsets():
+    """The pool holds more than 2^31 elements and the batch's pages lie at its
+    end."""
+    page, Hkv, D = 64, 8, 128
+    pages = 2 ** 31 // (page * Hkv * D) + 40
+    b = Batch(32, Hkv, D, BF, page, 300, [(9, 100), (4, 20)], seed=21)
+    far = torch.arange(b.k.shape[0], device="cuda") + pages - b.k.shape[0]
+    for name in ("k", "v"):
+        pool = torch.zeros((pages, page, Hkv, D), device="cuda", dtype=BF)
+        pool[far] = getattr(b, name)
+        setattr(b, name, pool)
+    shift = pages - far.numel()
+    b.prefix_pages = b.prefix_pages + shift
+    b.table = b.table + shift
+    b.check(True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,causal", [(128, True), (64, False)])
+def test_long_prompts(D, causal):
+    """Thousands of tokens against a thousand keys each: every row tile and
+    every tile of keys, by norms (the exact rows head by head)."""
+    b = Batch(8, 2, D, BF, 64, 200, [(1500, 1700), (3, 90), (700, 700)], seed=31)
+    got, lse = b.run(causal)
+    kp, vp = b.keys[0]
+    for r, (n, own) in enumerate(b.blocks):
+        t0 = b.start[r]
+        k, v = (torch.cat(x).double() for x in ((kp, b.keys[r + 1][0]), (vp, b.keys[r + 1][1])))
+        seen = 200 + (own - n + torch.arange(n, device="cuda") + 1 if causal else torch.full((n,), own, device="cuda"))
+        for h in range(8):
+            z = b.q[t0:t0 + n, h].double() @ k[:, h // 4].t() * D ** -0.5
+            z = z.masked_fill(torch.arange(k.shape[0], device="cuda") >= seen[:, None], float("-inf"))
+            want = z.softmax(-1) @ v[:, h // 4]
+            off = (got[t0:t0 + n, h].double() - want).norm(dim=-1) / want.norm(dim=-1)
+            # a row's error is a mean over D elements of two roundings of at most e/2
+            assert off.max() <= torch.finfo(BF).eps
+            assert (lse[t0:t0 + n, h].double() - torch.logsumexp(z, -1)).abs().max() <= 1e-4

@@ -203,3 +203,22 @@ def test_indexes_outside_their_tables():
         want = torch.tensor([1, 1, 0, 1, 1, 1, 0, 0], device="cuda").bfloat16()
         assert torch.equal(kc[:, 0, 0], want) and torch.equal(vc[:, 1, 5], want)
     assert ws.device_status() == (ops.MOE_OK, 0)
+
+
+@pytest.mark.gpu
+def test_slots_past_32_bit_offsets():
+    """Rows of a cache of more than 2^31 elements, and a projection row stride
+    that takes the last token past 2^31 elements of its tensor."""
+    Hkv, D = 8, 128
+    rows = 2 ** 31 // (Hkv * D) + 64
+    g = torch.Generator(device="cuda").manual_seed(8)
+    wide = torch.zeros((3, 2 ** 30 + 64), device="cuda", dtype=torch.bfloat16)
+    k = wide[:, :Hkv * D].unflatten(1, (Hkv, D))
+    k.copy_(torch.randn((3, Hkv, D), generator=g, device="cuda"))
+    table, pos = ops.rope_table(16, D), torch.tensor([3, 0, 15], device="cuda", dtype=torch.int32)
+    cache = torch.zeros((rows, Hkv, D), device="cuda", dtype=torch.bfloat16)
+    slots = torch.tensor([rows - 1, rows - 64, 5], device="cuda", dtype=torch.int32)
+    ws = ops.Workspace(ops.STATUS_BYTES)
+    ops.qk_norm_rope(None, k, None, pos, table, ws, k_cache=cache, slots=slots)
+    assert ws.device_status() == (ops.MOE_OK, 0)
+    _near(cache[slots.long()], *_formula(k, None, 0, table, pos, D, False), torch.bfloat16)
