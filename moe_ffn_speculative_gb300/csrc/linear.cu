@@ -1,8 +1,8 @@
 // Matrix product with bias, activation and residual in its epilogue
 // (moe_linear): y = act(x W^T + bias) + residual, W [N, K].
 //
-// Few rows: bound by the bytes of W, which are read once.  The 128 rows of a
-// weight tile are the MMA's M dimension and up to 256 tokens its N dimension;
+// Few rows (few_rows): bound by the bytes of W, which are read once.  The 128 rows of a
+// weight tile are the MMA's M dimension and up to 128 tokens its N dimension;
 // a cluster of CTAs shares a weight tile, each taking a range of K, so that a
 // layer with few tiles still occupies the SMs.  The CTAs' fp32 sums meet in
 // distributed shared memory: every CTA adds its share of the tokens over the
@@ -35,7 +35,7 @@ constexpr int kLinThreads = 192;
 // their first weights' way into L2) start while the previous kernel ends.
 constexpr int kLinSmem = 112 * 1024;
 constexpr int kLinMaxStages = 12;
-constexpr int kFewTokens = 128;          // up to this many rows: linear_few_kernel, one tile of tokens
+constexpr int kFewTokens = 128;          // most rows of linear_few_kernel, one tile of tokens
 constexpr int kMaxCluster = 8;
 
 struct LinearParams {
@@ -504,7 +504,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 }
 
 // Outputs of a tile: the width that makes the waves of tiles cheapest, a wave
-// costing its width and about 24 outputs' worth of fixed time.
+// costing its width and about 24 outputs' worth of fixed time.  us at the width
+// taken and at others: 256 x 4096 -> 6144: 96 15.5; 128 17.0, 192 20.2, 256 24.9.
+// 1001 x 2056 -> 5000: 144 30.3; 96 35.5, 192 34.3, 256 38.3.  4096 x 4096 ->
+// 12288: 256 230; 192 245, 144 270, 96 310.
 int tile_width(int M, int N, int pairs) {
   int best = kManyWide;
   long long cost = -1;
@@ -597,6 +600,15 @@ int cluster_size(int tiles, int k_blocks, int sms) {
   return c;
 }
 
+// Which kernel: the few rows' one streams every weight once but multiplies 128
+// weights with all rows in each CTA, so it pays while the rows are few or a
+// weight tile has a cluster to share the reading.  us, few / many, K = 4096:
+//   N = 24576 (no cluster)    33 rows 37.2 / 37.5    64 40.1 / 38.1   128 48.8 / 40.1
+//   N = 12288 (cluster of 2)  48 rows 19.9 / 21.7    72 21.5 / 22.0    96 24.1 / 22.5
+//   N =  6144 (4)             96 rows 14.2 / 14.6   112 14.9 / 14.9   128 15.7 / 15.2
+//   N =  4096 (7)             72 rows 10.3 / 13.1   112 12.1 / 13.3   128 12.9 / 13.3
+bool few_rows(int M, int cluster) { return M <= kFewTokens && M <= 32 + 16 * cluster; }
+
 template <bool kBf16>
 cudaError_t launch_few(const CUtensorMap& tm_w, const CUtensorMap& tm_x, const LinearParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
@@ -654,10 +666,10 @@ moe_status moe_linear(const void* x, long long x_stride, int M, int K, const voi
   memset(&p, 0, sizeof(p));
   p.M = M; p.N = N; p.K = K;
   p.k_blocks = ceil_div(K, kBlockK);
-  const bool few = M <= kFewTokens;
+  if (M <= kFewTokens) p.cluster = cluster_size(ceil_div(N, kHalfRows), p.k_blocks, sms);
+  const bool few = few_rows(M, p.cluster);
   if (few) {
     p.n_tok = ceil_div(M, 16) * 16;
-    p.cluster = cluster_size(ceil_div(N, kHalfRows), p.k_blocks, sms);
     p.stages = (kLinSmem - 1024) / (kTileBytesA + p.n_tok * 128);
     if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
     p.tmem_cols = 32;

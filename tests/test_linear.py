@@ -205,3 +205,17 @@ def test_tails_of_the_activations():
         y = ops.linear(x, w, ws, activation=act)
         assert bool(torch.isfinite(y).all())
         _check(x, w, None, act, None, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [19456, 12288, 8192, 6144, 264])
+@pytest.mark.parametrize("M", [33, 48, 49, 64, 65, 80, 81, 96, 97, 112, 113, 128, 129])
+def test_between_the_two_kernels(M, N):
+    """On both sides of the number of rows at which the kernel changes, with
+    the many rows' tiles less than half full."""
+    K = 264
+    x, w, b, r = _inputs(M, K, N, BF, True, True, seed=M)
+    ws = ops.Workspace(ops.linear_workspace_bytes(M, N, K))
+    y = ops.linear(x, w, ws, bias=b, activation="relu", residual=r)
+    assert ws.device_status() == (ops.MOE_OK, 0)
+    _check(x, w, b, "relu", r, y)
