@@ -105,8 +105,9 @@ struct Plan {
 // CTAs of phase 1.  A unit of it keeps a CTA busy for about 2500 clocks, one of
 // phase 2 (two slots at a time) for 0.75 as long and 0.028 more for every box
 // that a tile is copied in.  (64 requests over 16384 shared keys, pages of 64,
-// with a factor of 0.6, 0.8, 1: 182, 151, 170 us; draft blocks over 30011, pages
-// of 16: 87, 80, 77.)
+// 0.75 + 0.028 x 2 boxes: 153.7 us, 0.82 + 0.014 x: 155.4, 0.6 and 1 alone, before
+// the loads got faster: 182, 170.  Draft blocks over 30011, pages of 16: 64.6,
+// 65.7.)
 __device__ __forceinline__ int ctas_of_phase1(uint32_t units1, uint32_t units2, int ctas, int page) {
   if (units1 == 0) return 0;
   if (units2 == 0) return ctas;
@@ -386,6 +387,7 @@ constexpr int kSequence = 16;
 // four softmax warps) through a window of this many.
 constexpr int kSegments = 4;
 constexpr int kReaders = 6;
+constexpr int kPagesAtOnce = 8;  // pages whose copies are issued together
 
 struct Control {
   uint64_t q_full[2][2], q_empty[2][2];
@@ -426,9 +428,14 @@ __device__ __forceinline__ bool take(Control& c, int slot, int& n, Segment& s, i
 // Keys of tile j that some row of the segment sees.
 __device__ __forceinline__ int valid_keys(const Segment& s, int j) { return min(kTile, s.keys - j * kTile); }
 
-// ---------------------------------------------------------------- TMA producer (one thread of warp 0)
+// ---------------------------------------------------------------- TMA producer (warp 0)
+// The lanes wait and walk together; one of them issues.  A tile's pages are read
+// a lane each while the tile before is loaded, and go to the issuing lane by
+// shuffle, kPagesAtOnce before its copies.  (Draft blocks over pages of 16: 78.5,
+// 73.2, 67.2, 64.6 us with 1, 2, 4, 8; a single thread that read pages in pairs
+// ahead of their copies took 76.5.)
 // One copy of the load serves both slots, keys and values: a slot's state is
-// selected, not unrolled, since this thread is bound by fetching its code (with
+// selected, not unrolled, since this warp is bound by fetching its code (with
 // six inlined copies a load took it 1300 clocks, and the own keys' bandwidth
 // was that).
 template <int D>
@@ -445,19 +452,21 @@ struct Producer {
   Ring ring;
   int q_fills0, q_fills1;    // query tiles loaded so far, per slot
   int kv_fills0, kv_fills1;  // tiles announced so far, per slot
-  bool bad;                  // a page outside the cache was seen
+  int lane;
+  bool bad;                  // this lane saw a page outside the cache
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t info) {
-    if (mbar_wait(bar, parity, &c.abort_flag)) return true;
-    record_failure(p.status, &c.abort_flag, info);
-    return false;
+    return warp_wait(c, bar, parity, p.status, info);
   }
   // The slot's n-th segment, read where it lies until it is released.
   __device__ __forceinline__ const Segment* take(int slot, int n) {
     if (!wait(&c.seg_full[slot][n % kSegments], (n / kSegments) & 1, kInfoAttnList)) return nullptr;
     return &c.seg[slot][n % kSegments];
   }
-  __device__ __forceinline__ void release(int slot, int n) { mbar_arrive(&c.seg_empty[slot][n % kSegments]); }
+  __device__ __forceinline__ void release(int slot, int n) {
+    __syncwarp();
+    if (elect()) mbar_arrive(&c.seg_empty[slot][n % kSegments]);
+  }
   // Pages outside the cache become the first one past it: the copy fills zeros.
   __device__ __forceinline__ int page_at(const int32_t* pages, int i) {
     const uint32_t pg = static_cast<uint32_t>(__ldg(pages + i)), n = static_cast<uint32_t>(p.n_pages);
@@ -467,37 +476,37 @@ struct Producer {
   __device__ __forceinline__ int boxes(int keys, int j) const {
     return (min(kTile, keys - j * kTile) + box_rows - 1) / box_rows;
   }
-  // The first two pages of tile j.
-  __device__ __forceinline__ void first_pages(const Segment* s, int j, int& a, int& b) {
-    const int32_t* pages = s->pages + ((j * kTile) >> p.page_log2);
-    a = page_at(pages, 0);
-    b = boxes(s->keys, j) > 1 ? page_at(pages, 1) : 0;
+  // The pages of tile j, a lane each (pages have 8 keys or more: 16 at most).
+  __device__ __forceinline__ int pages_of(const Segment* s, int j) {
+    return lane < boxes(s->keys, j) ? page_at(s->pages + ((j * kTile) >> p.page_log2), lane) : 0;
   }
   // The next tile of `slot` (in phase 1, of both: announced to slot 0): a box
   // for each page and 64-column half.
-  __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment* s, int j, int slot, int a, int b) {
+  __device__ __forceinline__ bool load_kv(const CUtensorMap* tm, const Segment* s, int j, int slot, int pages) {
     if (!wait(&c.kv_empty[ring.stage], ring.phase ^ 1u, kInfoAttnStage)) return false;
     const int n = boxes(s->keys, j), h = s->h, fills = slot ? kv_fills1++ : kv_fills0++, entry = fills % kSequence;
     uint64_t* bar = &c.kv_full[slot][entry];
     uint8_t* dst = kv_mem + ring.stage * Geo::kTileBytes;
-    c.stage_of[slot][entry] = ring.stage;
-    mbar_arrive_expect_tx(bar, n * box_rows * D * 2);
+    if (elect()) {
+      c.stage_of[slot][entry] = ring.stage;
+      mbar_arrive_expect_tx(bar, n * box_rows * D * 2);
+    }
     const int row = (j * kTile) & (p.page - 1), step = box_rows * 128;
-    const int32_t* pages = s->pages + ((j * kTile) >> p.page_log2);
 #pragma unroll 1
-    for (int i = 0; i < n; i += 2) {
-      const int a1 = i + 2 < n ? page_at(pages, i + 2) : 0, b1 = i + 3 < n ? page_at(pages, i + 3) : 0;
+    for (int i = 0; i < n; i += kPagesAtOnce) {
+      int page[kPagesAtOnce];
 #pragma unroll
-      for (int half = 0; half < D / 64; ++half)
-        tma_load_4d(dst + half * (kTile * 128), tm, bar, half * 64, h, row, a);
-      if (i + 1 < n) {
+      for (int k = 0; k < kPagesAtOnce; ++k) page[k] = __shfl_sync(0xffffffffu, pages, i + k);
+      if (elect()) {
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half)
-          tma_load_4d(dst + half * (kTile * 128) + step, tm, bar, half * 64, h, row, b);
+        for (int k = 0; k < kPagesAtOnce; ++k) {
+          if (i + k >= n) break;
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half)
+            tma_load_4d(dst + half * (kTile * 128) + k * step, tm, bar, half * 64, h, row, page[k]);
+        }
       }
-      dst += 2 * step;
-      a = a1;
-      b = b1;
+      dst += kPagesAtOnce * step;
     }
     ring.next(room.stages);
     return true;
@@ -507,10 +516,12 @@ struct Producer {
     if (!wait(&c.q_empty[slot][buf], ((n / Geo::kQBufs) & 1) ^ 1u, kInfoAttnQuery)) return false;
     uint64_t* bar = &c.q_full[slot][buf];
     uint8_t* dst = q_mem + (slot * Geo::kQBufs + buf) * room.q_bytes;
-    mbar_arrive_expect_tx(bar, p.G * q_tokens * D * 2);
+    if (elect()) {
+      mbar_arrive_expect_tx(bar, p.G * q_tokens * D * 2);
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half)
-      tma_load_4d(dst + half * room.q_half, tm_q, bar, half * 64, 0, s->h, s->tok0);
+      for (int half = 0; half < D / 64; ++half)
+        tma_load_4d(dst + half * room.q_half, tm_q, bar, half * 64, 0, s->h, s->tok0);
+    }
     return true;
   }
 
@@ -519,19 +530,19 @@ struct Producer {
   // whose segments differ in their row tile only.
   __device__ __forceinline__ bool run(bool phase2) {
     int n0 = 0, n1 = 0, j0 = -1, j1 = -1;      // segment and tile of each slot (-1: none yet)
-    int a0 = 0, b0 = 0, a1 = 0, b1 = 0;        // the tile's first pages
+    int pages0 = 0, pages1 = 0;                // the tile's pages
     bool live0 = true, live1 = phase2;
 #pragma unroll 1
     for (int x = 0; live0 || live1; x = phase2 ? x ^ 1 : 0) {
       if (!(x ? live1 : live0)) continue;
-      int n = x ? n1 : n0, j = x ? j1 : j0, pa = x ? a1 : a0, pb = x ? b1 : b0;
+      int n = x ? n1 : n0, j = x ? j1 : j0;
       const Segment* s = &c.seg[x][n % kSegments];
       bool fresh = j < 0;
-      int na = 0, nb = 0;  // the next tile's pages, under way during this one's values
+      int next = 0;  // the next tile's pages, under way during this one's values
       if (!fresh) {
         const bool more = j + 1 < s->j1;
-        if (more) first_pages(s, j + 1, na, nb);
-        if (!load_kv(tm_v, s, j, x, pa, pb)) return false;
+        if (more) next = pages_of(s, j + 1);
+        if (!load_kv(tm_v, s, j, x, x ? pages1 : pages0)) return false;
         ++j;
         if (!more) {
           release(x, n);
@@ -548,17 +559,17 @@ struct Producer {
         ended = s->phase == 0;
         if (!ended) {
           j = s->j0;
-          first_pages(s, j, na, nb);
+          next = pages_of(s, j);
           if (!load_q(s, x) || (!phase2 && !load_q(other, 1))) return false;
         }
       }
-      if (!ended && !load_kv(tm_k, s, j, x, na, nb)) return false;
+      if (!ended && !load_kv(tm_k, s, j, x, next)) return false;
       if (bad) {
         bad = false;
         record_index(p.status, kInfoPage);
       }
-      if (x) { n1 = n; j1 = j; a1 = na; b1 = nb; live1 = !ended; }
-      else { n0 = n; j0 = j; a0 = na; b0 = nb; live0 = !ended; }
+      if (x) { n1 = n; j1 = j; pages1 = next; live1 = !ended; }
+      else { n0 = n; j0 = j; pages0 = next; live0 = !ended; }
     }
     return true;
   }
@@ -1028,12 +1039,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
-      if (elect()) {
-        Producer<D> r{p,    c,    q_mem, kv_mem, phase2 ? &tm_q2 : &tm_q, &tm_k, &tm_v, room, min(p.page, kTile),
-                      phase2 ? p.tpt2 : p.tpt, Ring(), 0, 0, 0, 0, false};
-        r.run(phase2);
-        r.drain();
-      }
+      Producer<D> r{p,    c,    q_mem, kv_mem, phase2 ? &tm_q2 : &tm_q, &tm_k, &tm_v, room, min(p.page, kTile),
+                    phase2 ? p.tpt2 : p.tpt, Ring(), 0, 0, 0, 0, lane, false};
+      r.run(phase2);
+      r.drain();
     } else if (warp <= 2) {
       const int slot = warp - 1;
       Issuer<kBf16, D> r{p, c, smem_u32(q_mem + slot * Geo::kQBufs * room.q_bytes) >> 4, smem_u32(kv_mem) >> 4,
