@@ -75,7 +75,7 @@ __device__ __forceinline__ float activate(float v, int act) {
     case MOE_ACT_GELU: return 0.5f * v * erfcf(-v * 0.70710678118654752f);
     case MOE_ACT_GELU_TANH:
       return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-    case MOE_ACT_RELU: return fmaxf(v, 0.f);
+    case MOE_ACT_RELU: return v <= 0.f ? 0.f : v;  // NaN stays NaN (fmaxf returns the other operand)
     default: return v;
   }
 }
