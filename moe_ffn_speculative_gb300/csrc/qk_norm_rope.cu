@@ -108,13 +108,15 @@ __device__ __forceinline__ Part from_pairs(const float (&a)[4], const float (&b)
 }
 
 // The rotation of a lane's pairs with the norm's weights in it:
-// (a, b) -> r (a ca - b sb, b cb + a sa).
+// (a, b) -> r (a ca - b sb, b cb + a sa); past the rotated part r (a ca, b cb),
+// without a product of the one with the other (0 times an infinity is NaN).
 template <bool kBf16, bool kInter, int D>
 struct Turn {
   float ca[4], sb[4], cb[4], sa[4];
-  bool norm;
-  __device__ __forceinline__ Turn(const float (&c)[4], const float (&s)[4], const uint16_t* weight, int ea, int eb) {
-    norm = weight != nullptr;
+  bool norm, rotated;
+  __device__ __forceinline__ Turn(const float (&c)[4], const float (&s)[4], bool rotated, const uint16_t* weight, int ea,
+                                  int eb)
+      : norm(weight != nullptr), rotated(rotated) {
     float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
     if (norm) to_pairs<kBf16, kInter>(load_part(weight, ea, eb), wa, wb);
 #pragma unroll
@@ -139,8 +141,8 @@ struct Turn {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      ya[i] = (a[i] * ca[i] - b[i] * sb[i]) * r;
-      yb[i] = (b[i] * cb[i] + a[i] * sa[i]) * r;
+      ya[i] = (rotated ? a[i] * ca[i] - b[i] * sb[i] : a[i] * ca[i]) * r;
+      yb[i] = (rotated ? b[i] * cb[i] + a[i] * sa[i] : b[i] * cb[i]) * r;
     }
     return from_pairs<kBf16, kInter>(ya, yb);
   }
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __g
     s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
   }
   {
-    const Turn<kBf16, kInter, D> turn(c, s, p.q_weight, ea, eb);
+    const Turn<kBf16, kInter, D> turn(c, s, lane < turning, p.q_weight, ea, eb);
     uint16_t* out = p.q_out + t * p.q_out_stride;
     for (int base = 0; base < p.Hq; base += groups * kHeads) {  // the same count in every lane
       if (base > 0) {
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __g
     }
   }
   if (p.Hkv == 0) return;
-  const Turn<kBf16, kInter, D> turn(c, s, p.k_weight, ea, eb);
+  const Turn<kBf16, kInter, D> turn(c, s, lane < turning, p.k_weight, ea, eb);
   for (int base = 0; base < p.Hkv; base += groups) {
     const int h = base + group;
     if (base > 0 && h < p.Hkv) {
