@@ -507,8 +507,8 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  *   seen = own_len where causal is 0 (every token of a draft block sees the
  *   whole block), else max(0, own_len - n + i + 1)
- * in fp32 (the probabilities enter the second product in the 16-bit type),
- * rounded once.  A token that sees no key, or that belongs to no request, gets
+ * in fp32 (the probabilities enter the second product in the 16-bit type; in
+ * f16 each to within 2^-32 of the row's largest), rounded once.  A token that sees no key, or that belongs to no request, gets
  * out = 0 and lse = -infinity.
  *   q            [T] rows of Hq x D, q_stride elements apart
  *   q_start      [B+1] int32: request b has the tokens [q_start[b],

@@ -6,9 +6,19 @@
 // prefix keys and the first `seen` of the request's own keys:
 //   o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),  s_j = scale log2(e) q . k_j,
 // computed over tiles of 128 keys with a running reference m and running sums
-// (fp32).  m is the row's maximum when it was last moved; it moves only when
-// a tile's maximum exceeds it by more than 8, so that the accumulator is
-// rarely rescaled and no power exceeds 2^8 (the ratio is exact whatever m is).
+// (fp32).  m is the row's maximum when it was last moved, less kLift; it moves
+// only when a tile's maximum exceeds that maximum by more than 8 (f16: 7), so that
+// the accumulator is rarely rescaled (the ratio is exact whatever m is).
+//
+// The powers enter the second product in the inputs' 16-bit type, as the MMA
+// takes both operands in one type: one rounding of at most e/2 each, independent
+// from key to key, beside the output's own (their sums l stay fp32, unrounded).
+// Held in two halves they would lose nothing, at half as much tensor time again.
+// bf16 has fp32's exponents.  f16 ends at 2^-24 and 65504, so there the maximum
+// counts 2^7 (kLift) and no power passes 2^14 (two more bits are left for the
+// rounding of logits past 2^24): a key is held to within 2^-32 of the row's
+// largest, however many there are.  (With the maximum at 1, the bound was 2^-25:
+// 131072 keys 17.4 nats below one lost all of their weight together, 0.36 %.)
 //
 // Work.  The G = Hq / Hkv heads of a token that read one key head are rows of
 // one product, so a row tile is floor(128 / G) tokens x G heads (in phase 2
@@ -55,7 +65,10 @@ namespace {
 constexpr int kTile = 128;           // keys of a tile, rows of a row tile
 constexpr int kAttnThreads = 384;    // 12 warps
 constexpr int kItemCost = 1;         // an item's fixed cost, in key tiles
-constexpr float kRescaleAt = 8.f;    // how far a tile's maximum may pass the reference (powers of two)
+// What the row's maximum counts when the reference is set, and how far a later
+// tile's maximum may pass that (powers of two).
+template <bool kBf16> constexpr float kLift = kBf16 ? 0.f : 7.f;
+template <bool kBf16> constexpr float kRescaleAt = kBf16 ? 8.f : 7.f;
 constexpr int kAttnSmem = 232448;    // 227 KB
 // Registers a thread: 384 x 168 at launch, moved from warps 0..3 to the
 // softmax warps, which hold a row's 128 scores (128 x (104 + 2 x 200) = 384 x 168)
@@ -800,9 +813,9 @@ struct Softmax {
       for (int i = 0; i < kTile; i += 2)
         top[(i / 2) % 4] = max3(top[(i / 2) % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-      const bool move = mt > m + kRescaleAt;  // also from -infinity
+      const bool move = mt > m + (kLift<kBf16> + kRescaleAt<kBf16>);  // also from -infinity
       if (__any_sync(0xffffffffu, move)) {
-        const float m1 = move ? mt : m;
+        const float m1 = move ? mt - kLift<kBf16> : m;
         const float a = move ? ex2(m - m1) : 1.f;
         m = m1;
         l *= a;
