@@ -97,7 +97,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !flat(kc, type, kc->numel()))
       Py_RETURN_NONE;
     n_slots = kc->numel() / (Hkv * D);
-    if (v && (!heads(*v, type, T, Hkv, D, vs) || !flat(vc, type, kc->numel()))) Py_RETURN_NONE;
+    if (v && (!heads(*v, type, T, Hkv, D, vs) || vc->dim() < 2 || vc->size(-1) != D || vc->size(-2) != Hkv ||
+              !flat(vc, type, kc->numel())))
+      Py_RETURN_NONE;
   }
   if (rope && (rope->dim() != 2 || !fits(rope->size(0)) || !flat(rope, at::kFloat, rope->numel()))) Py_RETURN_NONE;
   if (!flat(pos, at::kInt, T) || !flat(slots, at::kInt, T) || !flat(qw, type, D) || !flat(kw, type, D)) Py_RETURN_NONE;
@@ -132,7 +134,7 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t cap = pp ? pp->numel() : 0, width = table && table->dim() == 2 ? table->size(1) : 0;
   long long qs = 0;
   if (!heads(*q, type, T, Hq, D, qs) || kc->size(3) != D || !flat(kc, type, kc->numel()) ||
-      !flat(vc, type, kc->numel()) || B < 0 || (pp != nullptr) != (pl != nullptr) ||
+      !flat(vc, type, kc->numel()) || vc->sizes() != kc->sizes() || B < 0 || (pp != nullptr) != (pl != nullptr) ||
       (table != nullptr) != (own != nullptr) || (table && (table->dim() != 2 || table->size(0) != B)))
     Py_RETURN_NONE;
   if (!fits(T) || !fits(B) || !fits(pages) || !fits(page) || !fits(cap) || !fits(width) ||

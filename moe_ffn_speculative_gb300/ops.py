@@ -533,6 +533,8 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
         if v is not None:
             vs = _heads(v, dtype, T, Hkv, D, "v")
             pv = v.data_ptr()
+            if v_cache.shape[-2:] != (Hkv, D):
+                raise ValueError("v_cache: expected [..., Hkv, D]")
             pvc = _flat(v_cache, dtype, size, "v_cache")
     if (v is not None and k is None) or (v_cache is not None and v is None):
         raise ValueError("v needs k, v_cache needs v")
@@ -588,6 +590,8 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
     size = pages * page * Hkv * dk
     if dk != D:
         raise ValueError("caches: expected heads of q's size")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache: expected the shape of k_cache")
     B = q_start.numel() - 1
     if B < 0 or (prefix_pages is None) != (prefix_len is None) or (page_table is None) != (own_len is None):
         raise ValueError("q_start has B+1 elements; page lists come with their lengths")
