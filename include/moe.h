@@ -523,7 +523,9 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
  *                keys, likewise; table_width 0: none (then both may be NULL)
  *   out          [T, Hq, D], not q
  *   lse          [T, Hq] fp32 or NULL (natural logarithm)
- *   ws           >= moe_prefix_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes
+ *   ws           >= moe_prefix_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes,
+ *                asked for these T and B or for larger ones: the size serves
+ *                every call of fewer tokens and requests of the same heads
  * All lengths and tables stay on the device, so a captured call serves later
  * steps of the same T and B.  A page outside [0, n_pages) is recorded
  * (MOE_INFO_PAGE) and read as zeros; a length outside its table is recorded

@@ -56,6 +56,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "moe.h"
 #include "moe_internal.cuh"
 
@@ -1297,6 +1299,20 @@ AttnLayout attn_layout(int T, int B, int Hq, int Hkv, int D, int ctas) {
   return L;
 }
 
+// Bytes that serve every call of at most T tokens and B requests of these heads:
+// attn_layout with the terms that T, B and their ratio move either way (the pairs,
+// the last row tile's tokens) at their largest.
+size_t attn_bytes_upto(int T, int B, int Hq, int Hkv, int D, int ctas) {
+  const int tpt = kTile / (Hq / Hkv);
+  const size_t spare = 2ull * kTile * ctas;
+  const size_t rows1 = static_cast<size_t>(T) * Hq + spare;
+  const size_t rows2 = (static_cast<size_t>(T) + (T < tpt ? T : tpt)) * Hq + spare;
+  size_t o = kWsHeaderBytes + kWsAlign + ws_align_up(sizeof(RequestPlan) * static_cast<size_t>(B)) +
+             ws_align_up(4 * static_cast<size_t>(T));
+  for (const size_t rows : {rows1, rows2}) o += ws_align_up(8 * rows) + ws_align_up(4 * ((rows + 31) / 32 * 32) * D);
+  return o;
+}
+
 cudaError_t launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned grid, int threads, size_t smem,
                           cudaStream_t s) {
   memset(cfg, 0, sizeof(*cfg));
@@ -1348,7 +1364,7 @@ size_t moe_prefix_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D
   using namespace moe;
   if (shape_status(T, B, Hq, Hkv, D) != MOE_OK) return 0;
   const int sms = device_sms();
-  return sms > 0 ? attn_layout(T, B, Hq, Hkv, D, sms).total : 0;
+  return sms > 0 ? attn_bytes_upto(T, B, Hq, Hkv, D, sms) : 0;
 }
 
 moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B, const int32_t* q_start, int Hq,
