@@ -19,6 +19,10 @@
 // persistent; two accumulators in tensor memory let a tile's epilogue run
 // under the next tile's products.  The tile's width is chosen so that the last
 // wave of tiles is full.
+//
+// Neither kernel signals its dependents before it is complete, although its own
+// start may overlap its predecessor's end: y may be the expert weights of a fused
+// forward, which loads the first of them before it waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -31,8 +35,9 @@ namespace moe {
 namespace {
 
 constexpr int kLinThreads = 192;
-// Half an SM's shared memory: two CTAs are resident, so that a launch's CTAs (and
-// their first weights' way into L2) start while the previous kernel ends.
+// Half an SM's shared memory: two CTAs are resident, so that clusters of more CTAs
+// than there are SMs run at once, and, behind a kernel that signals its dependents
+// early, a launch's CTAs (and their first weights' way into L2) start while it ends.
 constexpr int kLinSmem = 112 * 1024;
 constexpr int kLinMaxStages = 12;
 constexpr int kFewTokens = 128;          // most rows of linear_few_kernel, one tile of tokens
@@ -136,7 +141,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  griddep_launch_dependents();
   // the weights' first tiles come into L2 while the previous kernel ends (what
   // it writes, weights included, is read only after it)
   if (warp == 0 && elect())
@@ -404,7 +408,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c.tmem;
   griddep_wait();
-  griddep_launch_dependents();
 
   if (warp == 0) {
     // this CTA's 128 token rows and its half of the tile's weight rows
@@ -505,9 +508,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
 // Outputs of a tile: the width that makes the waves of tiles cheapest, a wave
 // costing its width and about 24 outputs' worth of fixed time.  us at the width
-// taken and at others: 256 x 4096 -> 6144: 96 15.5; 128 17.0, 192 20.2, 256 24.9.
-// 1001 x 2056 -> 5000: 144 30.3; 96 35.5, 192 34.3, 256 38.3.  4096 x 4096 ->
-// 12288: 256 230; 192 245, 144 270, 96 310.
+// taken and at others: 256 x 4096 -> 6144: 96 16.4; 128 17.6, 192 20.8, 256 25.7.
+// 1001 x 2056 -> 5000: 144 31.1; 96 35.4, 192 35.7, 256 38.3.  4096 x 4096 ->
+// 12288: 256 227 to 236; 192 240, 144 260, 96 312.
 int tile_width(int M, int N, int pairs) {
   int best = kManyWide;
   long long cost = -1;
@@ -589,9 +592,9 @@ int resident_clusters(int c) {
 
 // CTAs that share a weight tile: as many as leave each at least 4 of the
 // 64-input k-blocks, make at most 1.5 CTAs an SM and are resident at once.  (72
-// x 4096 -> 6144, 48 tiles: 26.1, 15.4, 14.0, 12.6, 12.6, 19.4 us with 1 .. 6, of
-// which 6 no longer fit; 9 x 4096 -> 4096, 32 tiles: 16.4, 10.0, 8.7, 7.9, 8.4,
-// 8.1.)
+// x 4096 -> 6144, 48 tiles: 24.6, 16.5, 14.6, 13.4, 14.2, 19.7 us with 1 .. 6, of
+// which 6 no longer fit; 9 x 4096 -> 4096, 32 tiles: 16.9, 11.3, 9.9, 9.1, 9.5,
+// 9.2, and 9.1 with the 7 that it takes.)
 int cluster_size(int tiles, int k_blocks, int sms) {
   int c = 1;
   while (c < kMaxCluster && 2 * (c + 1) * tiles <= 3 * sms && k_blocks / (c + 1) >= 4 &&
@@ -603,10 +606,10 @@ int cluster_size(int tiles, int k_blocks, int sms) {
 // Which kernel: the few rows' one streams every weight once but multiplies 128
 // weights with all rows in each CTA, so it pays while the rows are few or a
 // weight tile has a cluster to share the reading.  us, few / many, K = 4096:
-//   N = 24576 (no cluster)    33 rows 37.2 / 37.5    64 40.1 / 38.1   128 48.8 / 40.1
-//   N = 12288 (cluster of 2)  48 rows 19.9 / 21.7    72 21.5 / 22.0    96 24.1 / 22.5
-//   N =  6144 (4)             96 rows 14.2 / 14.6   112 14.9 / 14.9   128 15.7 / 15.2
-//   N =  4096 (7)             72 rows 10.3 / 13.1   112 12.1 / 13.3   128 12.9 / 13.3
+//   N = 24576 (no cluster)    48 rows 38.2 / 38.6    64 40.3 / 39.0   128 50.7 / 41.1
+//   N = 12288 (cluster of 2)  64 rows 21.9 / 23.0    80 22.6 / 23.1    96 25.0 / 23.5
+//   N =  6144 (4)             96 rows 15.3 / 15.5   112 15.9 / 15.7   128 16.6 / 16.1
+//   N =  4096 (7)             72 rows 11.8 / 13.7   112 13.7 / 14.0   128 14.6 / 14.0
 bool few_rows(int M, int cluster) { return M <= kFewTokens && M <= 32 + 16 * cluster; }
 
 template <bool kBf16>
