@@ -531,7 +531,9 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
  * (MOE_INFO_PAGE) and read as zeros; a length outside its table is recorded
  * (MOE_INFO_LENGTH) and held within it; a request whose starts are out of
  * order or outside [0, T] is recorded (MOE_INFO_STARTS) and its tokens' output
- * is not defined.
+ * is not defined, nor is that of tokens that two requests claim; where the rest
+ * still claim more than T tokens together, no request is served (out = 0, lse =
+ * -infinity for every token).
  * Limits: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 128, Hq <= 1024;
  * page_size a power of two from 8 to 1024; T <= MOE_MAX_ATTN_TOKENS, B <=
  * MOE_MAX_REQUESTS, prefix_cap and table_width times page_size <=

@@ -150,6 +150,7 @@ __device__ __forceinline__ int held(int len, int pages, int page, int32_t* statu
 
 struct Request {
   int a, n, len;  // first token, tokens, own keys
+  bool ok;        // its starts are in order
   // keys seen by the last token of row tile rt
   __device__ int seen(const AttnParams& p, int rt) const {
     if (!p.causal) return len;
@@ -173,7 +174,8 @@ __device__ __noinline__ Request read_request(const AttnParams& p, int b) {
   const int z = __ldg(p.q_start + b + 1);
   r.n = z - r.a;
   r.len = p.table_width > 0 ? held(__ldg(p.own_len + b), p.table_width, p.page, p.status) : 0;
-  if (r.a < 0 || z < r.a || z > p.T) {
+  r.ok = r.a >= 0 && z >= r.a && z <= p.T;
+  if (!r.ok) {
     record_index(p.status, kInfoStarts);
     r.a = r.n = 0;
   }
@@ -198,6 +200,7 @@ struct Walker {
   uint32_t left;   // units still to walk
   int off;         // units of the current item before the share
   int h, i, rt;    // phase 1: h, pair i; phase 2: h, request i (-1: the prefix item), row tile rt
+  int batch;       // requests that are served
   Request rq;
   int prefix_len, prefix_tiles;
 
@@ -214,14 +217,15 @@ struct Walker {
   }
   // Phase 2, share w; the list position of its first unit was found by the
   // scan of the requests.
-  __device__ void begin2(const AttnParams& p, int plen, int w, uint32_t units, int head, int request, int skip) {
-    phase = 2; share = w; prefix_len = plen; prefix_tiles = tiles_of(plen);
+  __device__ void begin2(const AttnParams& p, int plen, int w, uint32_t units, int head, int request, int skip,
+                         int served) {
+    phase = 2; share = w; batch = served; prefix_len = plen; prefix_tiles = tiles_of(plen);
     left = units; h = head; i = request; rt = 0; off = skip;
     if (left > 0 && i >= 0) rq = read_request(p, i);
   }
   __device__ void next_request(const AttnParams& p) {
     rt = 0;
-    if (++i >= p.B) { i = -1; ++h; }
+    if (++i >= batch) { i = -1; ++h; }
     if (i >= 0) rq = read_request(p, i);
   }
   __device__ bool next(const AttnParams& p, Segment& s) {
@@ -422,6 +426,8 @@ struct Control {
   Shares s1;
   uint32_t units[2];
   int head[2], request[2], skip[2];
+  int batch;                       // requests that are served
+  unsigned long long claimed;      // tokens, where some starts are out of order
 };
 
 __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t parity, int32_t* status, int32_t info) {
@@ -886,22 +892,37 @@ struct Softmax {
 // ---------------------------------------------------------------- planner (warp 3)
 // Both slots' places in the phase 2 list: a scan over the requests' units by
 // the whole CTA (a warp alone takes longer even over 8 requests).  What
-// merge_kernel needs of it goes to the workspace.
+// merge_kernel needs of it goes to the workspace.  Starts out of order anywhere
+// may leave blocks that overlap: where they claim more than the T tokens that the
+// entry point counted units for, no request is served.
 __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int plen) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kAttnThreads / 32;
   const uint32_t lead = p.left ? units_of(tiles_of(plen)) : 0;  // the prefix item comes first
   uint32_t mine = 0, cost0 = 0;
+  int tokens = 0;  // (T of each of 65536 / 384 requests, at most)
+  bool ok = true;
   for (int b = tid; b < p.B; b += kAttnThreads) {
-    const uint32_t u = read_request(p, b).units(p);
+    const Request rq = read_request(p, b);
+    const uint32_t u = rq.units(p);
     if (b == tid) cost0 = u;
     mine += u;
+    tokens += rq.n;
+    ok &= rq.ok;
   }
   uint32_t all = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) c.sums[warp] = all;
-  __syncthreads();
+  int batch = p.B;
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) c.claimed = 0;
+    __syncthreads();
+    atomicAdd(&c.claimed, static_cast<unsigned long long>(tokens));
+    __syncthreads();
+    if (c.claimed > static_cast<unsigned long long>(p.T)) batch = 0;
+  }
   all = 0;
-  for (int w = 0; w < kWarps; ++w) all += c.sums[w];
+  if (batch > 0)
+    for (int w = 0; w < kWarps; ++w) all += c.sums[w];
   __syncthreads();
   const uint32_t per_head = lead + all, units1 = units_of(tiles_of(plen)) * p.pairs * p.Hkv;
   const int c1 = ctas_of_phase1(units1, per_head * p.Hkv, p.ctas, p.page);
@@ -927,12 +948,13 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
     c.s1 = s1;
     c.share = w0 < 0 ? static_cast<int>(blockIdx.x) : w0;
     c.phase = w0 < 0 ? 1 : 2;
+    c.batch = batch;
   }
   uint32_t base = lead;
   for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
     const int b = b0 + tid;
-    uint32_t own = cost0;
-    if (b0 > 0) own = b < p.B ? read_request(p, b).units(p) : 0;
+    uint32_t own = b < batch ? cost0 : 0;
+    if (b0 > 0) own = b < batch ? read_request(p, b).units(p) : 0;
     uint32_t inc = own;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -955,7 +977,7 @@ __device__ __forceinline__ void find_shares(const AttnParams& p, Control& c, int
       }
     if (b < p.B && b % p.ctas == static_cast<int>(blockIdx.x)) {
       const Request rq = read_request(p, b);
-      p.requests[b] = RequestPlan{rq.a, rq.n, rq.len, first};
+      p.requests[b] = RequestPlan{rq.a, b < batch ? rq.n : 0, rq.len, first};
     }
   }
 }
@@ -968,7 +990,8 @@ __device__ __forceinline__ void hand_list(const AttnParams& p, Control& c, int s
   int n = 0;
   bool have = false;
   if (c.phase == 1) w.begin1(p, plen, c.s1, c.share);
-  else w.begin2(p, plen, c.share + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot]);
+  else w.begin2(p, plen, c.share + slot, c.units[slot], c.head[slot], c.request[slot], c.skip[slot],
+               c.batch);
   long long t0 = clock64();
   while (true) {
     if (!have) {
@@ -1074,7 +1097,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       // the tokens' requests, for merge_kernel: every CTA writes some
 #pragma unroll 1
-      for (int b = blockIdx.x; b < p.B; b += p.ctas) {
+      for (int b = blockIdx.x; b < c.batch; b += p.ctas) {
         const Request rq = read_request(p, b);
         for (int t = lane; t < rq.n; t += 32) p.request_of[rq.a + t] = b;
       }
@@ -1135,7 +1158,7 @@ __global__ void __launch_bounds__(merge_threads(kWarps)) merge_kernel(const __gr
   // (a token outside every request reads what an earlier call left: checked)
   if (b >= 0 && b < p.B) rp = p.requests[b];
   const bool owned = t >= rp.a && t < rp.a + rp.n;
-  const Request rq = {rp.a, rp.n, rp.len};
+  const Request rq = {rp.a, rp.n, rp.len, true};
   Parts run[2];  // the prefix item's parts, the request's
   run[0].count = run[1].count = 0;
   if (owned && ptiles > 0) {
