@@ -478,7 +478,7 @@ MOE_API void moe_set_profile_events(void* const* events, int n_pairs);
  *                whose position is outside [0, max_pos) is recorded
  *                (MOE_INFO_POSITION) and skipped: nothing of it is written
  *   q_out        rows of Hq x D, q_out_stride elements apart; may be q itself
- *                with q's stride
+ *                with q's stride, else shares no element with q, k, v or the caches
  *   k_cache, v_cache [n_slots, Hkv, D]: a cache of pages is the same rows,
  *                slot = page * page_size + offset.  v and v_cache may both be
  *                NULL
@@ -521,7 +521,8 @@ MOE_API moe_status moe_qk_norm_rope(const void* q, long long q_stride, const voi
  *                prefix_cap 0: no prefix (then both may be NULL)
  *   page_table   [B, table_width] int32, own_len [B] int32: each request's own
  *                keys, likewise; table_width 0: none (then both may be NULL)
- *   out          [T, Hq, D], not q
+ *   out          [T, Hq, D]; neither it nor lse shares memory with q, the caches
+ *                or the other
  *   lse          [T, Hq] fp32 or NULL (natural logarithm)
  *   ws           >= moe_prefix_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes,
  *                asked for these T and B or for larger ones: the size serves
@@ -561,7 +562,8 @@ MOE_API moe_status moe_prefix_attention(const void* q, long long q_stride, int T
  *              0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))), silu v / (1 + e^-v)
  *   residual   [M] rows of N, residual_stride elements apart, or NULL; may be
  *              y itself with y's stride
- *   y          [M] rows of N, y_stride elements apart; overlaps neither x nor w
+ *   y          [M] rows of N, y_stride elements apart; shares no element with
+ *              what is read (but the residual's own)
  *   ws         >= moe_linear_workspace_bytes(M, N, K) bytes
  * Limits: N and K multiples of 8; M, N, K <= MOE_MAX_LINEAR; pointers 16-byte
  * aligned. */

@@ -419,6 +419,22 @@ bool encode_map_16(CUtensorMap* m, bool f16, const void* base, int rank, const u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool rows_meet(const RowSet& a, const RowSet& b) {
+  if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  // rows at one place (stride 0) are one row
+  const long long ra = a.stride == 0 ? 1 : a.rows, rb = b.stride == 0 ? 1 : b.rows;
+  const size_t na = static_cast<size_t>((ra - 1) * a.stride + a.width);
+  const size_t nb = static_cast<size_t>((rb - 1) * b.stride + b.width);
+  if (!overlaps(a.at, na, b.at, nb)) return false;
+  if (ra == 1 && rb == 1) return true;
+  if (ra > 1 && rb > 1 && a.stride != b.stride) return true;
+  const long long stride = ra > 1 ? a.stride : b.stride;
+  // b's place in the columns that begin with a's row
+  long long d = static_cast<long long>((reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at))) % stride;
+  if (d < 0) d += stride;
+  return d < a.width || d + b.width > stride;
+}
+
 moe_status route_check_args(const moe_bf16* x, int T, int H, const moe_bf16* gate, const moe_recipe* recipe,
                             const int32_t* topk_idx, const float* topk_w) {
   const moe_status st = check_recipe(recipe);

@@ -661,6 +661,11 @@ moe_status moe_linear(const void* x, long long x_stride, int M, int K, const voi
   if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(y))
     return MOE_ERR_INVALID_ARG;
   if (x_stride % 8 || y_stride % 8 || (residual && residual_stride % 8)) return MOE_ERR_UNSUPPORTED;
+  const RowSet out = {y, M, 2ll * N, 2 * y_stride};
+  if (rows_meet(out, {x, M, 2ll * K, 2 * x_stride}) || rows_meet(out, {w, 1, 2ll * N * K, 0}) ||
+      rows_meet(out, {bias, 1, 2ll * N, 0}) ||
+      (residual != y && rows_meet(out, {residual, M, 2ll * N, 2 * residual_stride})))
+    return MOE_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) % kWsAlign) != 0 || ws_bytes < MOE_STATUS_BYTES)
     return MOE_ERR_WORKSPACE;
   const int sms = device_sms();

@@ -388,6 +388,16 @@ int device_sms();
 bool encode_map_16(CUtensorMap* m, bool f16, const void* base, int rank, const uint64_t* dims,
                    const uint64_t* strides, const uint32_t* box);
 
+// Rows of `width` bytes, `stride` bytes apart (one row: a contiguous run).
+struct RowSet {
+  const void* at;
+  long long rows, width, stride;
+};
+// Whether two sets of rows share a byte.  Sets that lie in one another's gaps
+// (column slices of one buffer) do not; sets of different strides whose ranges
+// overlap are taken to.
+bool rows_meet(const RowSet& a, const RowSet& b);
+
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;
 // `done` is the kernel's own mask of the devices (the first 64) where that has
 // been said, as the call costs a small launch a tenth of its host time.

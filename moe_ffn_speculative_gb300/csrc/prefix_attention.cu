@@ -1421,6 +1421,11 @@ moe_status moe_prefix_attention(const void* q, long long q_stride, int T, int B,
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || q == out)
     return MOE_ERR_INVALID_ARG;
   if (q_stride % 8) return MOE_ERR_UNSUPPORTED;
+  const long long row = 2ll * Hq * D, pool = prefix_cap + table_width > 0 ? 2ll * n_pages * page_size * Hkv * D : 0;
+  const RowSet o = {out, 1, row * T, 0}, z = {lse, 1, 4ll * T * Hq, 0};
+  for (const RowSet& read : {RowSet{q, T, row, 2 * q_stride}, RowSet{k_cache, 1, pool, 0}, RowSet{v_cache, 1, pool, 0}})
+    if (rows_meet(o, read) || rows_meet(z, read)) return MOE_ERR_INVALID_ARG;
+  if (rows_meet(o, z)) return MOE_ERR_INVALID_ARG;
   // a workspace that cannot even hold the fixed header is refused before any device query
   if (!ws || (reinterpret_cast<uintptr_t>(ws) % kWsAlign) != 0 || ws_bytes < kWsHeaderBytes) return MOE_ERR_WORKSPACE;
   const int sms = device_sms();

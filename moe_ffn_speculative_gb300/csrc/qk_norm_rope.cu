@@ -295,6 +295,13 @@ extern "C" moe_status moe_qk_norm_rope(const void* q, long long q_stride, const 
       !aligned16(rope) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
     return MOE_ERR_INVALID_ARG;
   if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_out_stride % 8) return MOE_ERR_UNSUPPORTED;
+  const long long q_row = 2ll * Hq * D, k_row = 2ll * Hkv * D;
+  const RowSet qo = {q_out, T, q_row, 2 * q_out_stride}, kc = {k_cache, 1, k_row * n_slots, 0},
+               vc = {v_cache, 1, k_row * n_slots, 0};
+  if ((q_out == q && T > 1 ? q_stride != q_out_stride : q_out != q && rows_meet(qo, {q, T, q_row, 2 * q_stride})) ||
+      rows_meet(qo, {k, T, k_row, 2 * k_stride}) || rows_meet(qo, {v, T, k_row, 2 * v_stride}) || rows_meet(qo, kc) ||
+      rows_meet(qo, vc) || rows_meet(kc, vc))
+    return MOE_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) % kWsAlign) != 0 || ws_bytes < MOE_STATUS_BYTES)
     return MOE_ERR_WORKSPACE;
   RopeParams p;
