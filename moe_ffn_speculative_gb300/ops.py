@@ -463,6 +463,20 @@ def _heads(t: torch.Tensor, dtype, T: int, h: int, D: int, name: str) -> int:
     return s0 if T > 1 else h * D
 
 
+def _made(shape, like: torch.Tensor, stream) -> torch.Tensor:
+    """A buffer of `like`'s type for a call on `stream`: from that stream's memory,
+    since a block that the current stream's work still reads is free for the
+    current stream only; and kept, once dropped, until the current stream's work
+    of then has ended, as the caller reads it there."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=like.dtype, device=like.device)
+    t.record_stream(current)
+    return t
+
+
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, scale: float = 1.0,
                device=None) -> torch.Tensor:
     """Cosines and sines of every position for ``qk_norm_rope``: fp32
@@ -489,7 +503,7 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
     lead = q if q is not None else k
     if lead.is_cuda and (k is None) == (k_cache is None) and (v is None) == (v_cache is None):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _made(q.shape, q, stream)
         status = _binding().qk_norm_rope(q, k, v, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_cache,
                                          v_cache, slots, ws.ptr(), ws.nbytes, _stream(stream))
         if status == 0:
@@ -508,7 +522,7 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
         Hq = h
         qs = _heads(q, dtype, T, h, D, "q")
         if q_out is None:
-            q_out = torch.empty((T, h, D), dtype=dtype, device=q.device)
+            q_out = _made((T, h, D), q, stream)
             qos = h * D
         else:
             qos = _heads(q_out, dtype, T, h, D, "q_out")
@@ -522,9 +536,9 @@ def qk_norm_rope(q, k, v, positions, rope, ws: Workspace, q_weight=None, k_weigh
             if slots is not None:
                 raise ValueError("slots name rows of a cache: pass k_cache and v_cache")
             if k_cache is None:
-                k_cache = torch.empty((T, Hkv, D), dtype=dtype, device=k.device)
+                k_cache = _made((T, Hkv, D), k, stream)
             if v is not None and v_cache is None:
-                v_cache = torch.empty((T, Hkv, D), dtype=dtype, device=k.device)
+                v_cache = _made((T, Hkv, D), k, stream)
         size = k_cache.numel()
         if k_cache.shape[-2:] != (Hkv, D):
             raise ValueError("k_cache: expected [..., Hkv, D]")
@@ -570,7 +584,7 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
     None; scale 1/sqrt(D) unless given; lse fp32 [T,Hq] is written when given.
     -> out [T,Hq,D]."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _made(q.shape, q, stream)
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if not q.is_cuda:
@@ -648,7 +662,7 @@ def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=No
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("expected x [M, K], w [N, K]")
     if y is None:
-        y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+        y = _made((x.shape[0], w.shape[0]), x, stream)
     if not x.is_cuda:
         _refuse(x, x.dtype, "x")
     status = _binding().linear(x, w, bias, act, residual, y, ws.ptr(), ws.nbytes, _stream(stream))
