@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe.h"
@@ -42,7 +43,12 @@ double number(PyObject* o, bool& ok) {
 }
 cudaStream_t stream_of(PyObject* o, bool& ok) { return reinterpret_cast<cudaStream_t>(integer(o, ok)); }
 
-bool gpu(const Tensor& t, at::ScalarType type) { return t.is_cuda() && t.scalar_type() == type; }
+// The current device, on which a call launches; asked for once a call.
+thread_local at::DeviceIndex here = -1;
+void look_up_device() { here = c10::impl::VirtualGuardImpl(at::kCUDA).getDevice().index(); }
+bool gpu(const Tensor& t, at::ScalarType type) {
+  return t.is_cuda() && t.device().index() == here && t.scalar_type() == type;
+}
 // A contiguous tensor of n elements, or none.
 bool flat(const Tensor* t, at::ScalarType type, int64_t n) {
   return t == nullptr || (gpu(*t, type) && t->is_contiguous() && t->numel() == n);
@@ -82,6 +88,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* lead = q ? q : k;
   int code = 0;
   if (!ok || !lead || (a[8] != Py_True && a[8] != Py_False) || !type16(*lead, code) || lead->dim() != 3) Py_RETURN_NONE;
+  look_up_device();
   const at::ScalarType type = lead->scalar_type();
   const int64_t T = lead->size(0), D = lead->size(2), Hq = q ? q->size(1) : 0;
   long long qs = 0, ks = 0, vs = 0, qos = 0, n_slots = 0;
@@ -128,6 +135,7 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!ok || !q || !kc || !vc || !start || !out || (a[8] != Py_True && a[8] != Py_False) || !type16(*q, code) ||
       q->dim() != 3 || kc->dim() != 4)
     Py_RETURN_NONE;
+  look_up_device();
   const at::ScalarType type = q->scalar_type();
   const int64_t T = q->size(0), Hq = q->size(1), D = q->size(2), B = start->numel() - 1;
   const int64_t pages = kc->size(0), page = kc->size(1), Hkv = kc->size(2);
@@ -165,6 +173,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const cudaStream_t stream = stream_of(a[8], ok);
   int code = 0;
   if (!ok || !x || !w || !y || !type16(*x, code) || x->dim() != 2 || w->dim() != 2) Py_RETURN_NONE;
+  look_up_device();
   const at::ScalarType type = x->scalar_type();
   const int64_t M = x->size(0), K = x->size(1), N = w->size(0);
   long long xs = 0, ys = 0, rs = 0;

@@ -435,14 +435,20 @@ def _refuse(t, dtype, name: str) -> None:
         raise TypeError(f"{name}: expected a {dtype} tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: tensor is not on a CUDA device")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensor is not on the current CUDA device")
     raise ValueError(f"{name}: tensor is not contiguous")
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    return not t.is_cuda or t.get_device() != torch.cuda.current_device()
 
 
 def _flat(t: Optional[torch.Tensor], dtype, n: int, name: str) -> Optional[int]:
     """Address of a contiguous tensor of n elements, or None."""
     if t is None:
         return None
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or _elsewhere(t) or not t.is_contiguous():
         _refuse(t, dtype, name)
     if t.numel() != n:
         raise ValueError(f"{name}: expected {n} elements")
@@ -452,7 +458,7 @@ def _flat(t: Optional[torch.Tensor], dtype, n: int, name: str) -> Optional[int]:
 def _heads(t: torch.Tensor, dtype, T: int, h: int, D: int, name: str) -> int:
     """Row stride of a [T, h, D] tensor on the GPU whose rows may lie apart (a
     slice of a fused projection)."""
-    if t.dtype is not dtype or not t.is_cuda:
+    if t.dtype is not dtype or _elsewhere(t):
         _refuse(t, dtype, name)
     if t.shape != (T, h, D):
         raise ValueError(f"{name}: expected [{T}, {h}, {D}]")
@@ -468,7 +474,7 @@ def _made(shape, like: torch.Tensor, stream) -> torch.Tensor:
     since a block that the current stream's work still reads is free for the
     current stream only; and kept, once dropped, until the current stream's work
     of then has ended, as the caller reads it there."""
-    if stream is None or not like.is_cuda:
+    if stream is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
     current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
@@ -583,12 +589,12 @@ def prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, pag
     both None; page_table int32 [B, width] with own_len int32 [B], or both
     None; scale 1/sqrt(D) unless given; lse fp32 [T,Hq] is written when given.
     -> out [T,Hq,D]."""
+    if not q.is_cuda:
+        _refuse(q, q.dtype, "q")
     if out is None:
         out = _made(q.shape, q, stream)
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    if not q.is_cuda:
-        _refuse(q, q.dtype, "q")
     status = _binding().prefix_attention(q, k_cache, v_cache, q_start, prefix_pages, prefix_len, page_table, own_len,
                                          causal, scale, out, lse, ws.ptr(), ws.nbytes, _stream(stream))
     if status == 0:
@@ -642,7 +648,7 @@ def linear_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def _rows(t: torch.Tensor, dtype, m: int, n: int, name: str) -> int:
     """Row stride of an [m, n] matrix on the GPU whose rows may lie apart."""
-    if t.dtype is not dtype or not t.is_cuda:
+    if t.dtype is not dtype or _elsewhere(t):
         _refuse(t, dtype, name)
     if t.shape != (m, n):
         raise ValueError(f"{name}: expected [{m}, {n}]")
@@ -661,10 +667,10 @@ def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=No
         raise ValueError(f"unknown activation {activation!r}")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("expected x [M, K], w [N, K]")
-    if y is None:
-        y = _made((x.shape[0], w.shape[0]), x, stream)
     if not x.is_cuda:
         _refuse(x, x.dtype, "x")
+    if y is None:
+        y = _made((x.shape[0], w.shape[0]), x, stream)
     status = _binding().linear(x, w, bias, act, residual, y, ws.ptr(), ws.nbytes, _stream(stream))
     if status == 0:
         return y
