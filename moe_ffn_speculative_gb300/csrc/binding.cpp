@@ -9,6 +9,7 @@
 #include <ATen/core/Tensor.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "moe.h"
 
@@ -206,4 +207,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  // what it was compiled against, for the loader to compare
+  if (m && (PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0 ||
+            PyModule_AddIntConstant(m, "python_version", PY_VERSION_HEX >> 16) != 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

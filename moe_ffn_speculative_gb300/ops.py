@@ -10,6 +10,7 @@ import ctypes
 import importlib.util
 import os
 import re
+import sys
 from typing import Optional, Tuple
 
 import torch
@@ -412,8 +413,20 @@ def _binding():
         spec = importlib.util.spec_from_file_location("_binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        _same_versions(module)
         _binding_module = module
     return _binding_module
+
+
+def _same_versions(module) -> None:
+    """Raises unless the extension was compiled for this torch and this Python: it
+    reads their objects by their headers' layout."""
+    version = re.match(r"\d+\.\d+\.\d+", torch.__version__).group()
+    python = sys.hexversion >> 16
+    if module.torch_version != version or module.python_version != python:
+        raise RuntimeError(f"_binding.so was built for torch {module.torch_version}, Python {module.python_version:#x}; "
+                           f"this is torch {version}, Python {python:#x}: build it again with "
+                           "moe_ffn_speculative_gb300.build.build()")
 
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
