@@ -746,7 +746,6 @@ struct Issuer {
       if (cur.last) {
         if (!take(c, slot, n, u, p.status)) return false;
         j = u.j0;
-        if (cur.both && u.phase != 1 && slot == 1) seen = 0;
       }
       const bool more = u.phase != 0;
       if (more && !wait_keys(next, u, j)) return false;

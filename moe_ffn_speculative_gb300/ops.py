@@ -693,11 +693,7 @@ def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=No
     M, K = x.shape
     N = w.shape[0]
     xs = _rows(x, dtype, M, K, "x")
-    if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=x.device)
-        ys = N
-    else:
-        ys = _rows(y, dtype, M, N, "y")
+    ys = _rows(y, dtype, M, N, "y")
     rs, pr = 0, None
     if residual is not None:
         rs, pr = _rows(residual, dtype, M, N, "residual"), residual.data_ptr()
