@@ -244,7 +244,9 @@ MOE_API moe_status moe_ffn_forward(const moe_bf16* x, int T, int H, int I,
  *       leaves (when that kernel allows it, as this one does) and stream
  *       their first weights into shared memory and L2 there; everything
  *       they read that a kernel writes (x, the workspace) waits until the
- *       previous kernel has completed.  So a CTA of the launch may wait for
+ *       previous kernel has completed.  (A kernel that writes these weights
+ *       therefore must not signal its dependents before it has: none of this
+ *       library's does, moe_linear among them.)  So a CTA of the launch may wait for
  *       another to be placed (bounded, MOE_ERR_DEVICE_TIMEOUT on expiry): the
  *       grid assumes the SMs are not held by other work for long, and
  *       moe_set_launch_overlap(0) makes it a cooperative launch instead.

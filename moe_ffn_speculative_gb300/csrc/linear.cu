@@ -22,7 +22,9 @@
 //
 // Neither kernel signals its dependents before it is complete, although its own
 // start may overlap its predecessor's end: y may be the expert weights of a fused
-// forward, which loads the first of them before it waits.
+// forward, which loads the first of them before it waits.  For the same reason
+// the writers fence at their end, before the last CTA's exit lets a dependent
+// start (0.15 us of 9 for 9 rows, nothing of 229 for 4096).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     cluster_sync();  // the others have read this CTA's sums
   }
+  __threadfence();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -496,6 +499,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_remote(map_rank(&c.acc_empty[buf], 0));
     }
+    __threadfence();
   }
   tc_fence_before();
   __syncthreads();
