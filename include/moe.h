@@ -73,13 +73,16 @@ typedef enum {
   MOE_ERR_CUDA = 4,           /* a CUDA runtime call failed                  */
   MOE_ERR_DEVICE_TIMEOUT = 5, /* a bounded device-side wait ran out          */
   MOE_ERR_DEVICE_RANGE = 6,   /* an input outside the exact range of the FP4
-                                 path (a block scale, or x / h beyond f16);
-                                 recorded on the device, the output is not
-                                 exact                                       */
-  MOE_ERR_DEVICE_INDEX = 7     /* an index read on the device (a position, a
+                                 path (a block scale, or x / h beyond f16) or
+                                 of the 4-bit cache; recorded on the device,
+                                 the output is not exact                     */
+  MOE_ERR_DEVICE_INDEX = 7,    /* an index read on the device (a position, a
                                  cache slot, a page, a length) lies outside
                                  its table; recorded on the device, the access
                                  is not made                                 */
+  MOE_ERR_DEVICE_POOL = 8      /* a request needs a page and none is free;
+                                 recorded on the device, the request keeps what
+                                 it has                                      */
 } moe_status;
 
 typedef enum {
@@ -389,8 +392,8 @@ MOE_API moe_status moe_ffn_forward_mx(const moe_bf16* x, int T, int H, int I, co
 /* Synchronises `stream`, reads the device status word of a workspace used by
  * any entry point, and clears it.  Returns MOE_OK or the
  * first device-side error recorded (MOE_ERR_DEVICE_TIMEOUT,
- * MOE_ERR_DEVICE_RANGE from the FP4 path, or MOE_ERR_DEVICE_INDEX from the
- * attention side); *info_out (if not NULL) receives
+ * MOE_ERR_DEVICE_RANGE from the FP4 path and the 4-bit cache, MOE_ERR_DEVICE_INDEX
+ * from the attention side, or MOE_ERR_DEVICE_POOL); *info_out (if not NULL) receives
  * the kernel-specific detail word (for MOE_ERR_DEVICE_TIMEOUT: which wait
  * ran out; MOE_INFO_HOLD for the start gate below).
  *
@@ -462,6 +465,12 @@ MOE_API void moe_set_profile_events(void* const* events, int n_pairs);
 #define MOE_INFO_PAGE 19     /* a page outside [0, n_pages)                   */
 #define MOE_INFO_LENGTH 20   /* a length below 0 or past its page table       */
 #define MOE_INFO_STARTS 21   /* block starts out of order or outside [0, T]   */
+#define MOE_INFO_FORK 31     /* a pair of a fork that cannot be made          */
+#define MOE_INFO_KEEP 32     /* a kept offset out of order or outside its table */
+/* info word of MOE_ERR_DEVICE_RANGE from moe_kv4_write */
+#define MOE_INFO_KV_RANGE 30
+/* info word of MOE_ERR_DEVICE_POOL */
+#define MOE_INFO_POOL 33
 
 /* Norms of the query and key heads, the position rotation and the cache
  * write, in one launch.  For every head row x of D elements, in fp32:
@@ -579,6 +588,115 @@ MOE_API size_t moe_linear_workspace_bytes(int M, int N, int K);
 MOE_API moe_status moe_linear(const void* x, long long x_stride, int M, int K, const void* w, int N, int dtype,
                               const void* bias, int activation, const void* residual, long long residual_stride,
                               void* y, long long y_stride, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- The attention side in 4 bits, and the pages of its cache.  Conventions of
+ * the attention side.
+ *
+ * A kv4 cache holds keys and values as the experts' FP4 weights are held: e2m1
+ * codes with one e8m0 scale (value 2^(s-127)) per 32 channels.  It is uint8
+ * [n_pages, Hkv, page_size * (D + D / 16)]; the block of a page and a head holds
+ *   codes of its keys   [D/32][page_size][16]  (even channel in the low nibble)
+ *   codes of its values [D/32][page_size][16]
+ *   scales of its keys  [page_size][D/32]
+ *   scales of its values [page_size][D/32]
+ * so that a page is one run of bytes, as the page operators need it.
+ * Limits of every call: D 64 or 128; page_size a power of two from 8 to 1024;
+ * Hkv <= 1024; n_pages * page_size < 2^31; pointers 16-byte aligned. */
+
+/* Keys and values rounded into their slots.  A group of 32 channels takes the
+ * least scale s in [104, 140] with max|x| <= 6 * 2^(s-127), and the code nearest to
+ * x / 2^(s-127), ties to the even code.  Elements past 6 * 2^13 = 49152 become that
+ * and are recorded (MOE_ERR_DEVICE_RANGE, MOE_INFO_KV_RANGE); a group with an
+ * infinity or NaN is recorded and reads as NaN (scale 255).
+ *   k, v       [T] rows of Hkv x D, k_stride, v_stride elements apart
+ *   slots      [T] int32, slot = page * page_size + offset (distinct tokens, distinct
+ *              slots); negative: padding, not written; past the cache: recorded
+ *              (MOE_INFO_SLOT), not written.  NULL: token t goes to slot t
+ *   cache      shares no byte with what is read
+ *   ws         >= MOE_STATUS_BYTES bytes */
+MOE_API moe_status moe_kv4_write(const void* k, long long k_stride, const void* v, long long v_stride, int T, int Hkv,
+                                 int D, int dtype, const int32_t* slots, void* cache, int n_pages, int page_size,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Pages expanded to 16 bits: k, v [n, page_size, Hkv, D] (a cache as
+ * moe_prefix_attention takes it), each element exactly what its code stands for
+ * (bf16) or that rounded (f16, where it passes 65504).
+ *   pages      [n] int32; one outside [0, n_pages) is recorded (MOE_INFO_PAGE) and
+ *              read as zeros.  NULL: the first n pages (then n <= n_pages)
+ *   ws         >= MOE_STATUS_BYTES bytes */
+MOE_API moe_status moe_kv4_read(const void* cache, int n_pages, int page_size, int Hkv, int D, const int32_t* pages,
+                                int n, void* k, void* v, int dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Pages of a cache.  The state lies on the device: refs [n_pages] int32, how
+ * many page-table entries hold a page (0: free); page_table [B, table_width] int32,
+ * the entries past a request's pages unused (the calls leave -1); own_len [B]
+ * int32, its tokens (0: the row is free).  The page numbers are those of every pool
+ * (the key and value caches of all layers, say), whose pages are copied together.
+ * Free pages are taken from the lowest number, by the requests in order: the
+ * outcome depends on the state alone.  A captured call serves later steps.
+ * Limits: page_size a power of two from 8 to 1024, B <= MOE_MAX_REQUESTS,
+ * table_width * page_size <= MOE_MAX_KEYS, n_pages * page_size < 2^31, n_pools <=
+ * MOE_MAX_POOLS; pools are distinct, 16-byte aligned, and share no byte with the
+ * other arguments.
+ *   ws         >= moe_pages_workspace_bytes(B, n_pages) bytes (>= MOE_STATUS_BYTES for
+ *              moe_pages_compact) */
+#define MOE_MAX_POOLS 64
+#define MOE_MAX_BLOCK 1024
+#define MOE_POOL_ROWS 0 /* [n_pages, page_size] rows of row_bytes bytes, a multiple of 16 */
+#define MOE_POOL_KV4 1  /* a kv4 cache of `heads` key heads of head_dim channels          */
+typedef struct {
+  void* data;
+  int32_t format;   /* MOE_POOL_*                              */
+  int32_t heads;    /* MOE_POOL_KV4                            */
+  int32_t head_dim; /* MOE_POOL_KV4                            */
+  int64_t row_bytes; /* MOE_POOL_ROWS                          */
+} moe_page_pool;
+
+MOE_API size_t moe_pages_workspace_bytes(int B, int n_pages);
+
+/* Every request gets the pages of its new length: own_len = new_len.
+ *   1. Entries past the new length are given back (refs - 1, entry -1).
+ *   2. A request takes the pages that it lacks.  Where it goes on writing into a page
+ *      (its shorter length ends inside one) that another entry holds too, it takes a
+ *      page in that one's place and the contents are copied in every pool.
+ *   3. A request for which the free pages do not suffice, and every later one that
+ *      needs any, is recorded (MOE_ERR_DEVICE_POOL) and keeps its first
+ *      min(own_len, new_len) tokens.
+ * A length outside [0, table_width * page_size] is recorded (MOE_INFO_LENGTH) and its
+ * request left alone; an entry outside the pool, or a page that no one holds, is
+ * recorded (MOE_INFO_PAGE) and passed over.  new_len 0 frees a request; new_len may
+ * not be own_len itself. */
+MOE_API moe_status moe_pages_resize(int32_t* refs, int n_pages, int32_t* page_table, int B, int table_width,
+                                    int page_size, int32_t* own_len, const int32_t* new_len,
+                                    const moe_page_pool* pools, int n_pools, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/* Request dst[i] becomes a copy of request src[i]: it shares the pages that are full
+ * (refs + 1) and takes a page for the last one when that is not, copied in every
+ * pool.
+ *   src, dst   [n] int32, n <= B; a pair with a negative one is passed over.  A pair
+ *              outside the table, or whose dst has tokens or is an earlier pair's, is
+ *              recorded (MOE_INFO_FORK) and not made; nor is one for which no page is
+ *              free (MOE_ERR_DEVICE_POOL), or a later one that needs any */
+MOE_API moe_status moe_pages_fork(int32_t* refs, int n_pages, int32_t* page_table, int B, int table_width,
+                                  int page_size, int32_t* own_len, const int32_t* src, const int32_t* dst, int n,
+                                  const moe_page_pool* pools, int n_pools, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/* Kept tokens of a block move up, in every pool: of request b, whose block (a tree of
+ * drafts, say) begins at token base[b], the row of token base[b] + keep[b][j] goes to token base[b] +
+ * j, for j up to the first negative entry; new_len[b] = base[b] + their number (what
+ * moe_pages_resize takes next).  A page that another request holds too must not be
+ * among those moved into (moe_pages_resize to the block's end sees to it).
+ *   keep       [B, n] int32, n <= MOE_MAX_BLOCK, growing; an entry that does not grow, or
+ *              whose row or place is outside the table or the pool, is recorded
+ *              (MOE_INFO_KEEP) and ends the list
+ *   base       [B] int32; one outside the table is recorded (MOE_INFO_LENGTH), nothing
+ *              moves
+ *   new_len    [B] int32 or NULL */
+MOE_API moe_status moe_pages_compact(const int32_t* page_table, int n_pages, int B, int table_width, int page_size,
+                                     const int32_t* base, const int32_t* keep, int n, const moe_page_pool* pools,
+                                     int n_pools, int32_t* new_len, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

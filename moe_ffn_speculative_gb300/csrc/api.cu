@@ -461,6 +461,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT";
     case MOE_ERR_DEVICE_RANGE: return "MOE_ERR_DEVICE_RANGE";
     case MOE_ERR_DEVICE_INDEX: return "MOE_ERR_DEVICE_INDEX";
+    case MOE_ERR_DEVICE_POOL: return "MOE_ERR_DEVICE_POOL";
   }
   return "MOE_ERR_UNKNOWN";
 }

@@ -187,6 +187,169 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+// A kv4 cache uint8 [pages, Hkv, page_size * (D + D / 16)]; its page size.
+bool kv4(const Tensor& t, int64_t D, int64_t& page) {
+  if (!gpu(t, at::kByte) || t.dim() != 3 || !t.is_contiguous() || D < 16 || D % 16 != 0) return false;
+  page = t.size(2) / (D + D / 16);
+  return fits(t.size(0)) && fits(t.size(1)) && fits(page) && page * (D + D / 16) == t.size(2);
+}
+
+// (k, v, slots, cache, workspace address, workspace bytes, stream)
+PyObject* kv4_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 7;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *k = tensor(a[0], ok), *v = tensor(a[1], ok), *slots = tensor(a[2], ok), *cache = tensor(a[3], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[4], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[5], ok));
+  const cudaStream_t stream = stream_of(a[6], ok);
+  int code = 0;
+  if (!ok || !k || !v || !cache || !type16(*k, code) || k->dim() != 3) Py_RETURN_NONE;
+  look_up_device();
+  const at::ScalarType type = k->scalar_type();
+  const int64_t T = k->size(0), Hkv = k->size(1), D = k->size(2);
+  int64_t page = 0;
+  long long ks = 0, vs = 0;
+  if (!fits(T) || !heads(*k, type, T, Hkv, D, ks) || !heads(*v, type, T, Hkv, D, vs) || !kv4(*cache, D, page) ||
+      cache->size(1) != Hkv || !flat(slots, at::kInt, T))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(moe_kv4_write(data(k), ks, data(v), vs, static_cast<int>(T), static_cast<int>(Hkv),
+                                       static_cast<int>(D), code, static_cast<const int32_t*>(data(slots)),
+                                       data(cache), static_cast<int>(cache->size(0)), static_cast<int>(page), ws,
+                                       ws_bytes, stream));
+}
+
+// (cache, head size, pages, k, v, workspace address, workspace bytes, stream)
+PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 8;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *cache = tensor(a[0], ok), *pages = tensor(a[2], ok), *k = tensor(a[3], ok), *v = tensor(a[4], ok);
+  const long long D = integer(a[1], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[5], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[6], ok));
+  const cudaStream_t stream = stream_of(a[7], ok);
+  int code = 0;
+  if (!ok || !cache || !k || !v || !type16(*k, code)) Py_RETURN_NONE;
+  look_up_device();
+  int64_t page = 0;
+  if (!kv4(*cache, D, page)) Py_RETURN_NONE;
+  const int64_t Hkv = cache->size(1), count = pages ? pages->numel() : cache->size(0);
+  const auto shaped = [&](const Tensor& t) {
+    return t.dim() == 4 && t.size(0) == count && t.size(1) == page && t.size(2) == Hkv && t.size(3) == D &&
+           flat(&t, k->scalar_type(), t.numel());
+  };
+  if (!fits(count) || !flat(pages, at::kInt, count) || !shaped(*k) || !shaped(*v)) Py_RETURN_NONE;
+  return PyLong_FromLong(moe_kv4_read(data(cache), static_cast<int>(cache->size(0)), static_cast<int>(page),
+                                      static_cast<int>(Hkv), static_cast<int>(D),
+                                      static_cast<const int32_t*>(data(pages)), static_cast<int>(count), data(k),
+                                      data(v), code, ws, ws_bytes, stream));
+}
+
+// The pools of a page call, of n_pages pages each: [n_pages, page_size, ...] rows
+// of any type, or a kv4 cache (uint8 of three dimensions).
+bool pools_of(PyObject* o, int64_t n_pages, int64_t page, moe_page_pool* out, int& n) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) > MOE_MAX_POOLS || page < 1) return false;
+  n = static_cast<int>(PyTuple_GET_SIZE(o));
+  for (int i = 0; i < n; ++i) {
+    bool ok = true;
+    const Tensor* t = tensor(PyTuple_GET_ITEM(o, i), ok);
+    if (!ok || !t || !t->is_cuda() || t->device().index() != here || t->dim() < 3 || !t->is_contiguous() ||
+        t->size(0) != n_pages)
+      return false;
+    moe_page_pool& p = out[i];
+    p = moe_page_pool{t->data_ptr(), MOE_POOL_ROWS, 0, 0, 0};
+    if (t->scalar_type() == at::kByte && t->dim() == 3) {
+      if (t->size(2) % page != 0 || t->size(2) / page * 16 % 17 != 0 || !fits(t->size(1))) return false;
+      p.format = MOE_POOL_KV4;
+      p.heads = static_cast<int32_t>(t->size(1));
+      p.head_dim = static_cast<int32_t>(t->size(2) / page * 16 / 17);
+    } else {
+      if (t->size(1) != page) return false;
+      p.row_bytes = t->element_size();
+      for (int64_t d = 2; d < t->dim(); ++d) p.row_bytes *= t->size(d);
+    }
+  }
+  return true;
+}
+
+// (refs, page_table, own_len, new_len, page_size, pools, workspace address,
+//  workspace bytes, stream)
+PyObject* pages_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 9;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *refs = tensor(a[0], ok), *table = tensor(a[1], ok), *own = tensor(a[2], ok), *now = tensor(a[3], ok);
+  const long long page = integer(a[4], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[6], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[7], ok));
+  const cudaStream_t stream = stream_of(a[8], ok);
+  if (!ok || !refs || !table || !own || !now || table->dim() != 2 || !fits(page)) Py_RETURN_NONE;
+  look_up_device();
+  const int64_t B = table->size(0), width = table->size(1), pages = refs->numel();
+  moe_page_pool pools[MOE_MAX_POOLS];
+  int n_pools = 0;
+  if (!fits(B) || !fits(width) || !fits(pages) || !flat(refs, at::kInt, pages) || !flat(table, at::kInt, B * width) ||
+      !flat(own, at::kInt, B) || !flat(now, at::kInt, B) || !pools_of(a[5], pages, page, pools, n_pools))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(moe_pages_resize(static_cast<int32_t*>(data(refs)), static_cast<int>(pages),
+                                          static_cast<int32_t*>(data(table)), static_cast<int>(B),
+                                          static_cast<int>(width), static_cast<int>(page),
+                                          static_cast<int32_t*>(data(own)), static_cast<const int32_t*>(data(now)),
+                                          pools, n_pools, ws, ws_bytes, stream));
+}
+
+// (refs, page_table, own_len, src, dst, page_size, pools, workspace address,
+//  workspace bytes, stream)
+PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 10;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *refs = tensor(a[0], ok), *table = tensor(a[1], ok), *own = tensor(a[2], ok), *src = tensor(a[3], ok),
+               *dst = tensor(a[4], ok);
+  const long long page = integer(a[5], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[7], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[8], ok));
+  const cudaStream_t stream = stream_of(a[9], ok);
+  if (!ok || !refs || !table || !own || !src || !dst || table->dim() != 2 || !fits(page)) Py_RETURN_NONE;
+  look_up_device();
+  const int64_t B = table->size(0), width = table->size(1), pages = refs->numel(), pairs = src->numel();
+  moe_page_pool pools[MOE_MAX_POOLS];
+  int n_pools = 0;
+  if (!fits(B) || !fits(width) || !fits(pages) || !fits(pairs) || !flat(refs, at::kInt, pages) ||
+      !flat(table, at::kInt, B * width) || !flat(own, at::kInt, B) || !flat(src, at::kInt, pairs) ||
+      !flat(dst, at::kInt, pairs) || !pools_of(a[6], pages, page, pools, n_pools))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(moe_pages_fork(
+      static_cast<int32_t*>(data(refs)), static_cast<int>(pages), static_cast<int32_t*>(data(table)),
+      static_cast<int>(B), static_cast<int>(width), static_cast<int>(page), static_cast<int32_t*>(data(own)),
+      static_cast<const int32_t*>(data(src)), static_cast<const int32_t*>(data(dst)), static_cast<int>(pairs), pools,
+      n_pools, ws, ws_bytes, stream));
+}
+
+// (page_table, base, keep, page_size, pages of the pools, pools, new_len,
+//  workspace address, workspace bytes, stream)
+PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 10;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *table = tensor(a[0], ok), *base = tensor(a[1], ok), *keep = tensor(a[2], ok), *now = tensor(a[6], ok);
+  const long long page = integer(a[3], ok), pages = integer(a[4], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[7], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[8], ok));
+  const cudaStream_t stream = stream_of(a[9], ok);
+  if (!ok || !table || !base || !keep || table->dim() != 2 || keep->dim() != 2 || !fits(page) || !fits(pages))
+    Py_RETURN_NONE;
+  look_up_device();
+  const int64_t B = table->size(0), width = table->size(1), block = keep->size(1);
+  moe_page_pool pools[MOE_MAX_POOLS];
+  int n_pools = 0;
+  if (!fits(B) || !fits(width) || !fits(block) || keep->size(0) != B || !flat(table, at::kInt, B * width) ||
+      !flat(base, at::kInt, B) || !flat(keep, at::kInt, B * block) || !flat(now, at::kInt, B) ||
+      !pools_of(a[5], pages, page, pools, n_pools))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(moe_pages_compact(static_cast<const int32_t*>(data(table)), static_cast<int>(pages),
+                                           static_cast<int>(B), static_cast<int>(width), static_cast<int>(page),
+                                           static_cast<const int32_t*>(data(base)),
+                                           static_cast<const int32_t*>(data(keep)), static_cast<int>(block), pools,
+                                           n_pools, static_cast<int32_t*>(data(now)), ws, ws_bytes, stream));
+}
+
 // No C++ exception leaves for the interpreter (a sparse tensor's layout throws
 // where its strides are asked for).
 typedef PyObject* Fast(PyObject*, PyObject* const*, Py_ssize_t);
@@ -202,6 +365,11 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {{"qk_norm_rope", FAST(qk_norm_rope), METH_FASTCALL, nullptr},
                          {"prefix_attention", FAST(prefix_attention), METH_FASTCALL, nullptr},
                          {"linear", FAST(linear), METH_FASTCALL, nullptr},
+                         {"kv4_write", FAST(kv4_write), METH_FASTCALL, nullptr},
+                         {"kv4_read", FAST(kv4_read), METH_FASTCALL, nullptr},
+                         {"pages_resize", FAST(pages_resize), METH_FASTCALL, nullptr},
+                         {"pages_fork", FAST(pages_fork), METH_FASTCALL, nullptr},
+                         {"pages_compact", FAST(pages_compact), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -19,7 +19,7 @@ namespace moe {
 // ----------------------------------------------------------------------------
 // status word (first 8 bytes of every workspace): {code, info}
 // ----------------------------------------------------------------------------
-enum : int32_t { kStatusTimeout = 5, kStatusRange = 6, kStatusIndex = 7 };
+enum : int32_t { kStatusTimeout = 5, kStatusRange = 6, kStatusIndex = 7, kStatusPool = 8 };
 // info values: which wait ran out
 enum : int32_t {
   kInfoEmpty = 1, kInfoFull = 2, kInfoAccFull = 3, kInfoAccEmpty = 4,
@@ -41,7 +41,10 @@ enum : int32_t {
   // scores, the probabilities, the output tile, copies or MMAs in flight, the
   // lists of segments, a slot's turn to issue
   kInfoAttnStage = 22, kInfoAttnQuery = 23, kInfoAttnScores = 24, kInfoAttnProbs = 25, kInfoAttnOut = 26,
-  kInfoAttnDrain = 27, kInfoAttnList = 28, kInfoAttnTurn = 29
+  kInfoAttnDrain = 27, kInfoAttnList = 28, kInfoAttnTurn = 29,
+  // a group of keys or values outside the 4-bit cache's range; a pair of a fork or
+  // an offset of a compaction outside its table; no free page (kStatusPool)
+  kInfoKvRange = 30, kInfoFork = 31, kInfoKeep = 32, kInfoPool = 33
 };
 
 // ----------------------------------------------------------------------------

@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT,
- MOE_ERR_DEVICE_RANGE, MOE_ERR_DEVICE_INDEX) = range(8)
+ MOE_ERR_DEVICE_RANGE, MOE_ERR_DEVICE_INDEX, MOE_ERR_DEVICE_POOL) = range(9)
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRTSOFTPLUS = 0, 1, 2
 # the workspace's start gate (include/moe.h) and the info word of its timeout
 WS_HOLD_OFFSET = 8
@@ -29,6 +29,7 @@ INFO_HOLD = 15
 # outside its table (include/moe.h)
 STATUS_BYTES = 256
 INFO_POSITION, INFO_SLOT, INFO_PAGE, INFO_LENGTH, INFO_STARTS = 17, 18, 19, 20, 21
+INFO_KV_RANGE, INFO_FORK, INFO_KEEP, INFO_POOL = 30, 31, 32, 33
 DTYPE_BF16, DTYPE_F16 = 0, 1
 # routed-expert formats of the block-scaled path
 FMT_FP4, FMT_FP8 = 1, 2
@@ -108,6 +109,12 @@ _SIGS = {
                                   _P, _P, _P, _SZ, _P]),
     "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_linear": (_I, [_P, _L, _I, _I, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _SZ, _P]),
+    "moe_kv4_write": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P]),
+    "moe_kv4_read": (_I, [_P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _SZ, _P]),
+    "moe_pages_workspace_bytes": (_SZ, [_I, _I]),
+    "moe_pages_resize": (_I, [_P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _SZ, _P]),
+    "moe_pages_fork": (_I, [_P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _I, _P, _SZ, _P]),
+    "moe_pages_compact": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P, _SZ, _P]),
 }
 
 SCHEDULE_AUTO, SCHEDULE_STREAM_K, SCHEDULE_SLICE = 0, 1, 2
@@ -434,6 +441,8 @@ _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 def _dtype16(t: torch.Tensor) -> int:
     """The library's code of a call's one 16-bit type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a tensor")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("expected a bfloat16 or float16 tensor")
@@ -702,6 +711,186 @@ def linear(x, w, ws: Workspace, bias=None, activation: str = "none", residual=No
     if status:
         raise MoeError(status, "moe_linear")
     return y
+
+
+# --------------------------------------------------------------------------- the attention side in 4 bits, pages
+#
+# As above: the extension module answers None where something is wrong with the
+# arguments, and the checks below say what.
+
+def _wrong(where: str) -> ValueError:
+    return ValueError(f"{where}: the arguments do not fit together")
+
+
+def _contiguous(t, dtype, name: str) -> None:
+    """Raises unless `t` is a contiguous tensor of `dtype` on the current GPU."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or _elsewhere(t) or not t.is_contiguous():
+        _refuse(t, dtype, name)
+
+
+def kv4_shape(pages: int, page_size: int, Hkv: int, D: int) -> Tuple[int, int, int]:
+    """Shape of a cache in 4 bits (uint8): e2m1 codes of keys and values with an
+    e8m0 scale per 32 channels (moe_kv4_write has the layout of a block)."""
+    return pages, Hkv, page_size * (D + D // 16)
+
+
+def _kv4_page(cache, D: int) -> int:
+    """Page size of a kv4 cache of heads of D channels."""
+    _contiguous(cache, torch.uint8, "cache")
+    slot = D + D // 16
+    if cache.dim() != 3 or slot == 0 or cache.shape[2] % slot:
+        raise ValueError(f"cache: expected [pages, Hkv, page_size * {slot}] (kv4_shape)")
+    return cache.shape[2] // slot
+
+
+def kv4_write(k, v, slots, cache, ws: Workspace, stream=None):
+    """Keys and values rounded to 4 bits into their slots of a cache
+    (moe_kv4_write).
+
+    k, v [T,Hkv,D] (rows may lie apart); slots int32 [T] (page * page_size +
+    offset; negative: padding; None: token t goes to slot t); cache uint8 of
+    ``kv4_shape``.  -> cache."""
+    status = _binding().kv4_write(k, v, slots, cache, ws.ptr(), ws.nbytes, _stream(stream))
+    if status == 0:
+        return cache
+    if status is not None:
+        raise MoeError(status, "moe_kv4_write")
+    _dtype16(k)
+    if k.dim() != 3:
+        raise ValueError("k: expected [T, heads, D]")
+    T, Hkv, D = k.shape
+    _heads(k, k.dtype, T, Hkv, D, "k")
+    _heads(v, k.dtype, T, Hkv, D, "v")
+    _kv4_page(cache, D)
+    if cache.shape[1] != Hkv:
+        raise ValueError("cache: expected the heads of k")
+    _flat(slots, torch.int32, T, "slots")
+    raise _wrong("kv4_write")
+
+
+def kv4_read(cache, D: int, ws: Workspace, pages=None, k=None, v=None, dtype=torch.bfloat16, stream=None):
+    """Pages of a 4-bit cache expanded to 16 bits (moe_kv4_read): pages int32 [n]
+    (None: all).  -> k, v [n, page_size, Hkv, D], of `dtype` where they are not
+    given."""
+    page = _kv4_page(cache, D)
+    n = cache.shape[0] if pages is None else pages.numel()
+    like = cache.new_empty(0, dtype=dtype) if k is None or v is None else None
+    k = _made((n, page, cache.shape[1], D), like, stream) if k is None else k
+    v = _made((n, page, cache.shape[1], D), like, stream) if v is None else v
+    status = _binding().kv4_read(cache, D, pages, k, v, ws.ptr(), ws.nbytes, _stream(stream))
+    if status == 0:
+        return k, v
+    if status is not None:
+        raise MoeError(status, "moe_kv4_read")
+    _dtype16(k)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape != (n, page, cache.shape[1], D):
+            raise ValueError(f"{name}: expected [n, page_size, Hkv, D]")
+        _contiguous(t, k.dtype, name)
+    _flat(pages, torch.int32, n, "pages")
+    raise _wrong("kv4_read")
+
+
+def pages_workspace_bytes(B: int, n_pages: int) -> int:
+    n = lib().moe_pages_workspace_bytes(B, n_pages)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_pages_workspace_bytes")
+    return n
+
+
+def _check_pools(caches, n_pages: int, page_size: int) -> None:
+    """Says what keeps the caches from being pools of n_pages pages."""
+    if len(caches) > 64:
+        raise ValueError("caches: at most 64")
+    for i, t in enumerate(caches):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"caches[{i}]: expected a tensor")
+        _contiguous(t, t.dtype, f"caches[{i}]")
+        if t.dim() < 3 or t.shape[0] != n_pages:
+            raise ValueError(f"caches[{i}]: expected {n_pages} pages")
+        kv4 = t.dtype is torch.uint8 and t.dim() == 3
+        if kv4 and (t.shape[2] % page_size or t.shape[2] // page_size * 16 % 17):
+            raise ValueError(f"caches[{i}]: expected [pages, Hkv, page_size * (D + D / 16)]")
+        if not kv4 and t.shape[1] != page_size:
+            raise ValueError(f"caches[{i}]: expected [pages, page_size, ...]")
+
+
+def _check_page_state(refs, page_table, own_len, page_size: int, caches) -> None:
+    _contiguous(refs, torch.int32, "refs")
+    _contiguous(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected [B, width]")
+    _flat(own_len, torch.int32, page_table.shape[0], "own_len")
+    if page_size < 1:
+        raise ValueError("page_size: expected a positive number")
+    _check_pools(caches, refs.numel(), page_size)
+
+
+def pages_resize(refs, page_table, own_len, new_len, page_size: int, ws: Workspace, caches=(), stream=None) -> None:
+    """Gives every request the pages of its new length and takes back the others
+    (moe_pages_resize); 0 frees a request.
+
+    refs int32 [pages], page_table int32 [B, width] and own_len int32 [B] are the
+    state, changed in place; new_len int32 [B]; caches: the tensors whose pages these
+    are, [pages, page_size, ...] or of ``kv4_shape``, in which a page that is written
+    on while another request shares it is copied."""
+    caches = tuple(caches)
+    status = _binding().pages_resize(refs, page_table, own_len, new_len, page_size, caches, ws.ptr(), ws.nbytes,
+                                     _stream(stream))
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_pages_resize")
+    _check_page_state(refs, page_table, own_len, page_size, caches)
+    _contiguous(new_len, torch.int32, "new_len")
+    _flat(new_len, torch.int32, page_table.shape[0], "new_len")
+    raise _wrong("pages_resize")
+
+
+def pages_fork(refs, page_table, own_len, src, dst, page_size: int, ws: Workspace, caches=(), stream=None) -> None:
+    """Makes request dst[i] a copy of request src[i] (moe_pages_fork): full pages are
+    shared, the last one is copied in every cache.  src, dst int32 [n]; the rest as in
+    ``pages_resize``."""
+    caches = tuple(caches)
+    status = _binding().pages_fork(refs, page_table, own_len, src, dst, page_size, caches, ws.ptr(), ws.nbytes,
+                                   _stream(stream))
+    if status == 0:
+        return
+    if status is not None:
+        raise MoeError(status, "moe_pages_fork")
+    _check_page_state(refs, page_table, own_len, page_size, caches)
+    _contiguous(src, torch.int32, "src")
+    _contiguous(dst, torch.int32, "dst")
+    _flat(dst, torch.int32, src.numel(), "dst")
+    raise _wrong("pages_fork")
+
+
+def pages_compact(page_table, base, keep, page_size: int, ws: Workspace, caches=(), new_len=None, stream=None):
+    """Moves the kept tokens of every request's block up in every cache
+    (moe_pages_compact): token base[b] + keep[b, j] goes to base[b] + j.
+
+    base int32 [B], keep int32 [B, n] (growing offsets, the first negative one ends a
+    row); caches as in ``pages_resize``.  -> new_len int32 [B], the length after them."""
+    caches = tuple(caches)
+    if new_len is None:
+        new_len = _made(base.shape, base, stream)
+    n_pages = caches[0].shape[0] if caches else (2 ** 31 - 1) // max(1, page_size)
+    status = _binding().pages_compact(page_table, base, keep, page_size, n_pages, caches, new_len, ws.ptr(), ws.nbytes,
+                                      _stream(stream))
+    if status == 0:
+        return new_len
+    if status is not None:
+        raise MoeError(status, "moe_pages_compact")
+    _contiguous(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or keep.dim() != 2 or keep.shape[0] != page_table.shape[0]:
+        raise ValueError("expected page_table [B, width], keep [B, n]")
+    _contiguous(keep, torch.int32, "keep")
+    for t, name in ((base, "base"), (new_len, "new_len")):
+        _flat(t, torch.int32, page_table.shape[0], name)
+    if page_size < 1:
+        raise ValueError("page_size: expected a positive number")
+    _check_pools(caches, n_pages, page_size)
+    raise _wrong("pages_compact")
 
 
 def set_schedule(schedule: int) -> None:
