@@ -627,6 +627,26 @@ MOE_API moe_status moe_kv4_write(const void* k, long long k_stride, const void* 
 MOE_API moe_status moe_kv4_read(const void* cache, int n_pages, int page_size, int Hkv, int D, const int32_t* pages,
                                 int n, void* k, void* v, int dtype, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* moe_prefix_attention() over a kv4 cache: the same requests, prefix, tables, lengths,
+ * outputs, errors and limits, but for
+ *   cache      uint8 [n_pages, Hkv, page_size * (D + D / 16)], codes and scales as
+ *              moe_kv4_write writes them (scales in [104, 140], or 255); slots that no
+ *              length covers may hold anything, covered ones hold finite values
+ *   ws         >= moe_prefix_attention_kv4_workspace_bytes(T, B, Hq, Hkv, D) bytes,
+ *              asked for these T and B or for larger ones
+ *   limits     Hq / Hkv <= 64; Hq <= 1024
+ * The keys and values enter both products exactly, in f16; a bf16 query row is scaled
+ * by a power of two first, and its elements are held to 2^-40 of its largest (exact
+ * down to 2^-31 of it); the probabilities enter in f16, each to within 2^-32 of the
+ * row's largest. */
+MOE_API size_t moe_prefix_attention_kv4_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+MOE_API moe_status moe_prefix_attention_kv4(const void* q, long long q_stride, int T, int B, const int32_t* q_start,
+                                            int Hq, int Hkv, int D, int dtype, const void* cache, int n_pages,
+                                            int page_size, const int32_t* prefix_pages, int prefix_cap,
+                                            const int32_t* prefix_len, const int32_t* page_table, int table_width,
+                                            const int32_t* own_len, int causal, float scale, void* out, float* lse,
+                                            void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---- Pages of a cache.  The state lies on the device: refs [n_pages] int32, how
  * many page-table entries hold a page (0: free); page_table [B, table_width] int32,
  * the entries past a request's pages unused (the calls leave -1); own_len [B]

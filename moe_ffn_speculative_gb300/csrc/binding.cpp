@@ -244,6 +244,45 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                       data(v), code, ws, ws_bytes, stream));
 }
 
+// (q, cache, q_start, prefix_pages, prefix_len, page_table, own_len, causal,
+//  scale, out, lse, workspace address, workspace bytes, stream)
+PyObject* prefix_attention_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 14;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *q = tensor(a[0], ok), *cache = tensor(a[1], ok), *start = tensor(a[2], ok), *pp = tensor(a[3], ok),
+               *pl = tensor(a[4], ok), *table = tensor(a[5], ok), *own = tensor(a[6], ok), *out = tensor(a[9], ok),
+               *lse = tensor(a[10], ok);
+  const double scale = number(a[8], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[11], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[12], ok));
+  const cudaStream_t stream = stream_of(a[13], ok);
+  int code = 0;
+  if (!ok || !q || !cache || !start || !out || (a[7] != Py_True && a[7] != Py_False) || !type16(*q, code) ||
+      q->dim() != 3)
+    Py_RETURN_NONE;
+  look_up_device();
+  const at::ScalarType type = q->scalar_type();
+  const int64_t T = q->size(0), Hq = q->size(1), D = q->size(2), B = start->numel() - 1;
+  const int64_t cap = pp ? pp->numel() : 0, width = table && table->dim() == 2 ? table->size(1) : 0;
+  int64_t page = 0;
+  long long qs = 0;
+  if (!heads(*q, type, T, Hq, D, qs) || !kv4(*cache, D, page) || B < 0 || (pp != nullptr) != (pl != nullptr) ||
+      (table != nullptr) != (own != nullptr) || (table && (table->dim() != 2 || table->size(0) != B)))
+    Py_RETURN_NONE;
+  if (!fits(T) || !fits(B) || !fits(cap) || !fits(width) || !flat(start, at::kInt, B + 1) || !flat(pp, at::kInt, cap) ||
+      !flat(pl, at::kInt, 1) || !flat(table, at::kInt, B * width) || !flat(own, at::kInt, B) || out->dim() != 3 ||
+      out->size(0) != T || out->size(1) != Hq || !flat(out, type, T * Hq * D) || !flat(lse, at::kFloat, T * Hq))
+    Py_RETURN_NONE;
+  const moe_status st = moe_prefix_attention_kv4(
+      data(q), qs, static_cast<int>(T), static_cast<int>(B), static_cast<const int32_t*>(data(start)),
+      static_cast<int>(Hq), static_cast<int>(cache->size(1)), static_cast<int>(D), code, data(cache),
+      static_cast<int>(cache->size(0)), static_cast<int>(page), static_cast<const int32_t*>(data(pp)),
+      static_cast<int>(cap), static_cast<const int32_t*>(data(pl)), static_cast<const int32_t*>(data(table)),
+      static_cast<int>(width), static_cast<const int32_t*>(data(own)), a[7] == Py_True ? 1 : 0,
+      static_cast<float>(scale), data(out), static_cast<float*>(data(lse)), ws, ws_bytes, stream);
+  return PyLong_FromLong(st);
+}
+
 // The pools of a page call, of n_pages pages each: [n_pages, page_size, ...] rows
 // of any type, or a kv4 cache (uint8 of three dimensions).
 bool pools_of(PyObject* o, int64_t n_pages, int64_t page, moe_page_pool* out, int& n) {
@@ -367,6 +406,7 @@ PyMethodDef methods[] = {{"qk_norm_rope", FAST(qk_norm_rope), METH_FASTCALL, nul
                          {"linear", FAST(linear), METH_FASTCALL, nullptr},
                          {"kv4_write", FAST(kv4_write), METH_FASTCALL, nullptr},
                          {"kv4_read", FAST(kv4_read), METH_FASTCALL, nullptr},
+                         {"prefix_attention_kv4", FAST(prefix_attention_kv4), METH_FASTCALL, nullptr},
                          {"pages_resize", FAST(pages_resize), METH_FASTCALL, nullptr},
                          {"pages_fork", FAST(pages_fork), METH_FASTCALL, nullptr},
                          {"pages_compact", FAST(pages_compact), METH_FASTCALL, nullptr},

@@ -111,6 +111,9 @@ _SIGS = {
     "moe_linear": (_I, [_P, _L, _I, _I, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _SZ, _P]),
     "moe_kv4_write": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P]),
     "moe_kv4_read": (_I, [_P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _SZ, _P]),
+    "moe_prefix_attention_kv4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_prefix_attention_kv4": (_I, [_P, _L, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P, _I, _P, _I, _F, _P,
+                                      _P, _P, _SZ, _P]),
     "moe_pages_workspace_bytes": (_SZ, [_I, _I]),
     "moe_pages_resize": (_I, [_P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _SZ, _P]),
     "moe_pages_fork": (_I, [_P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _P, _I, _P, _SZ, _P]),
@@ -789,6 +792,53 @@ def kv4_read(cache, D: int, ws: Workspace, pages=None, k=None, v=None, dtype=tor
         _contiguous(t, k.dtype, name)
     _flat(pages, torch.int32, n, "pages")
     raise _wrong("kv4_read")
+
+
+def prefix_attention_kv4_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    n = lib().moe_prefix_attention_kv4_workspace_bytes(T, B, Hq, Hkv, D)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_prefix_attention_kv4_workspace_bytes")
+    return n
+
+
+def prefix_attention_kv4(q, cache, q_start, prefix_pages, prefix_len, page_table, own_len, ws: Workspace,
+                         causal: bool = True, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """``prefix_attention`` over a cache in 4 bits (moe_prefix_attention_kv4): cache
+    uint8 of ``kv4_shape``, the other arguments as there.  -> out [T,Hq,D]."""
+    if not q.is_cuda:
+        _refuse(q, q.dtype, "q")
+    if out is None:
+        out = _made(q.shape, q, stream)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    status = _binding().prefix_attention_kv4(q, cache, q_start, prefix_pages, prefix_len, page_table, own_len, causal,
+                                             scale, out, lse, ws.ptr(), ws.nbytes, _stream(stream))
+    if status == 0:
+        return out
+    if status is not None:
+        raise MoeError(status, "moe_prefix_attention_kv4")
+    _dtype16(q)
+    if q.dim() != 3:
+        raise ValueError("expected q [T, Hq, D]")
+    T, Hq, D = q.shape
+    _heads(q, q.dtype, T, Hq, D, "q")
+    _kv4_page(cache, D)
+    B = q_start.numel() - 1
+    if B < 0 or (prefix_pages is None) != (prefix_len is None) or (page_table is None) != (own_len is None):
+        raise ValueError("q_start has B+1 elements; page lists come with their lengths")
+    if page_table is not None and (page_table.dim() != 2 or page_table.shape[0] != B):
+        raise ValueError("page_table: expected [B, width]")
+    if out.shape != q.shape:
+        raise ValueError("out: expected the shape of q")
+    i32 = torch.int32
+    for t, n, name in ((q_start, B + 1, "q_start"), (prefix_len, 1, "prefix_len"), (own_len, B, "own_len")):
+        _flat(t, i32, n, name)
+    for t, name in ((prefix_pages, "prefix_pages"), (page_table, "page_table")):
+        if t is not None:
+            _contiguous(t, i32, name)
+    _contiguous(out, q.dtype, "out")
+    _flat(lse, torch.float32, T * Hq, "lse")
+    raise _wrong("prefix_attention_kv4")
 
 
 def pages_workspace_bytes(B: int, n_pages: int) -> int:
