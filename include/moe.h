@@ -592,7 +592,36 @@ MOE_API moe_status moe_linear(const void* x, long long x_stride, int M, int K, c
 /* ---- The attention side in 4 bits, and the pages of its cache.  Conventions of
  * the attention side.
  *
- * A kv4 cache holds keys and values as the experts' FP4 weights are held: e2m1
+ * Weights of 4 bits: w[n, k] = scales[n, k / group] * (code[n, k] - zero[n, k / group]),
+ * codes and zeros whole numbers 0 .. 15 (zero 8 where there are none), scales in the
+ * call's 16-bit type.
+ *   codes      [N, K/2] uint8, the even input in the low nibble, 16-byte aligned
+ *   scales     [N, K/group]      zeros [N, K/group] uint8 or NULL
+ * Limits: N a multiple of 8, K of group, group 32, 64 or 128; N, K <= MOE_MAX_LINEAR. */
+
+/* Bytes of a set of weights laid out for moe_linear_q4 (0 for an unsupported shape). */
+MOE_API size_t moe_q4_weight_bytes(int N, int K, int group, int has_zeros);
+
+/* Lays the weights out, once a set (load time); asynchronous on `stream`.
+ *   weights    >= moe_q4_weight_bytes() bytes, 16-byte aligned, owned by the caller and
+ *              passed to every moe_linear_q4() with these weights
+ * Returns MOE_ERR_WORKSPACE when weight_bytes is too small. */
+MOE_API moe_status moe_q4_prepare(const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int group,
+                                  void* weights, size_t weight_bytes, cudaStream_t stream);
+
+/* moe_linear() with such weights: y_m = act(x_m W^T + bias) + residual_m, the weights as
+ * they are (none is rounded), fp32 sums, one rounding.
+ *   weights    from moe_q4_prepare() with this N, K, group and (has_zeros) zeros or none,
+ *              and scales of this dtype
+ *   ws         >= moe_linear_q4_workspace_bytes(M, N, K) bytes
+ * The other arguments, limits and errors as in moe_linear(). */
+MOE_API size_t moe_linear_q4_workspace_bytes(int M, int N, int K);
+MOE_API moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const void* weights,
+                                 size_t weight_bytes, int N, int group, int has_zeros, int dtype, const void* bias,
+                                 int activation, const void* residual, long long residual_stride, void* y,
+                                 long long y_stride, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* A kv4 cache holds keys and values as the experts' FP4 weights are held: e2m1
  * codes with one e8m0 scale (value 2^(s-127)) per 32 channels.  It is uint8
  * [n_pages, Hkv, page_size * (D + D / 16)]; the block of a page and a head holds
  *   codes of its keys   [D/32][page_size][16]  (even channel in the low nibble)

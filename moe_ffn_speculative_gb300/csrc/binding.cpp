@@ -187,6 +187,34 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+// (x, prepared weights, N, K, group, zeros, bias, activation code, residual, y,
+//  workspace address, workspace bytes, stream)
+PyObject* linear_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  bool ok = n == 13;
+  if (!ok) Py_RETURN_NONE;
+  const Tensor *x = tensor(a[0], ok), *w = tensor(a[1], ok), *bias = tensor(a[6], ok), *res = tensor(a[8], ok),
+               *y = tensor(a[9], ok);
+  const long long N = integer(a[2], ok), K = integer(a[3], ok), group = integer(a[4], ok), act = integer(a[7], ok);
+  void* ws = reinterpret_cast<void*>(integer(a[10], ok));
+  const size_t ws_bytes = static_cast<size_t>(integer(a[11], ok));
+  const cudaStream_t stream = stream_of(a[12], ok);
+  int code = 0;
+  if (!ok || !x || !w || !y || (a[5] != Py_True && a[5] != Py_False) || !type16(*x, code) || x->dim() != 2) Py_RETURN_NONE;
+  look_up_device();
+  const at::ScalarType type = x->scalar_type();
+  const int64_t M = x->size(0);
+  long long xs = 0, ys = 0, rs = 0;
+  if (!fits(M) || !fits(K) || !fits(N) || !fits(act) || !fits(group) || !rows(*x, type, M, K, xs) ||
+      !flat(w, at::kByte, w->numel()) || !rows(*y, type, M, N, ys) || !flat(bias, type, N) ||
+      (res && !rows(*res, type, M, N, rs)))
+    Py_RETURN_NONE;
+  const moe_status st = moe_linear_q4(data(x), xs, static_cast<int>(M), static_cast<int>(K), data(w),
+                                      static_cast<size_t>(w->numel()), static_cast<int>(N), static_cast<int>(group),
+                                      a[5] == Py_True ? 1 : 0, code, data(bias), static_cast<int>(act), data(res), rs,
+                                      data(y), ys, ws, ws_bytes, stream);
+  return PyLong_FromLong(st);
+}
+
 // A kv4 cache uint8 [pages, Hkv, page_size * (D + D / 16)]; its page size.
 bool kv4(const Tensor& t, int64_t D, int64_t& page) {
   if (!gpu(t, at::kByte) || t.dim() != 3 || !t.is_contiguous() || D < 16 || D % 16 != 0) return false;
@@ -404,6 +432,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {{"qk_norm_rope", FAST(qk_norm_rope), METH_FASTCALL, nullptr},
                          {"prefix_attention", FAST(prefix_attention), METH_FASTCALL, nullptr},
                          {"linear", FAST(linear), METH_FASTCALL, nullptr},
+                         {"linear_q4", FAST(linear_q4), METH_FASTCALL, nullptr},
                          {"kv4_write", FAST(kv4_write), METH_FASTCALL, nullptr},
                          {"kv4_read", FAST(kv4_read), METH_FASTCALL, nullptr},
                          {"prefix_attention_kv4", FAST(prefix_attention_kv4), METH_FASTCALL, nullptr},

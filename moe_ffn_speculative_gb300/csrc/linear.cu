@@ -31,6 +31,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "epilogue.cuh"
 #include "moe.h"
 #include "moe_internal.cuh"
 
@@ -64,55 +65,12 @@ struct LinearControl {
   int abort_flag;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ float to_f(uint16_t u) {
-  if (kBf16) return __bfloat162float(__ushort_as_bfloat16(u));
-  return __half2float(__ushort_as_half(u));
-}
-template <bool kBf16>
-__device__ __forceinline__ uint16_t from_f(float v) {
-  if (kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  return __half_as_ushort(__float2half_rn(v));
-}
-
-// v sigmoid(v) and the like through one exponential (the quotient is 0 where it
-// has run over); erfc keeps gelu's negative tail from cancelling.
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case MOE_ACT_SILU: return __fdividef(v, 1.f + __expf(-v));
-    case MOE_ACT_GELU: return 0.5f * v * erfcf(-v * 0.70710678118654752f);
-    case MOE_ACT_GELU_TANH:
-      return __fdividef(v, 1.f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-    case MOE_ACT_RELU: return v <= 0.f ? 0.f : v;  // NaN stays NaN (fmaxf returns the other operand)
-    default: return v;
-  }
-}
-
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1)
                : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t local, uint32_t rank) {
-  uint32_t a;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-
 template <bool kBf16>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,

@@ -109,6 +109,10 @@ _SIGS = {
                                   _P, _P, _P, _SZ, _P]),
     "moe_linear_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_linear": (_I, [_P, _L, _I, _I, _P, _I, _I, _P, _I, _P, _L, _P, _L, _P, _SZ, _P]),
+    "moe_q4_weight_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_q4_prepare": (_I, [_P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "moe_linear_q4_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_linear_q4": (_I, [_P, _L, _I, _I, _P, _SZ, _I, _I, _I, _I, _P, _I, _P, _L, _P, _L, _P, _SZ, _P]),
     "moe_kv4_write": (_I, [_P, _L, _P, _L, _I, _I, _I, _I, _P, _P, _I, _I, _P, _SZ, _P]),
     "moe_kv4_read": (_I, [_P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _SZ, _P]),
     "moe_prefix_attention_kv4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
@@ -729,6 +733,77 @@ def _contiguous(t, dtype, name: str) -> None:
     """Raises unless `t` is a contiguous tensor of `dtype` on the current GPU."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or _elsewhere(t) or not t.is_contiguous():
         _refuse(t, dtype, name)
+
+
+class Q4Weight:
+    """Weights of 4 bits as ``q4_prepare`` lays them out: N outputs, K inputs, groups
+    of `group` inputs with scales of `dtype` and zero points or none."""
+
+    def __init__(self, data, N: int, K: int, group: int, dtype, zeros: bool):
+        self.data, self.N, self.K, self.group, self.dtype, self.zeros = data, N, K, group, dtype, zeros
+
+
+def q4_prepare(codes, scales, zeros=None, stream=None) -> Q4Weight:
+    """Lays out weights of 4 bits for ``linear_q4`` (moe_q4_prepare), once a set:
+    codes uint8 [N, K/2] (the even input in the low nibble), scales [N, K/group] of the
+    activations' type, zeros uint8 [N, K/group] or None (8 everywhere); the weight is
+    scale * (code - zero)."""
+    _contiguous(codes, torch.uint8, "codes")
+    _dtype16(scales)
+    _contiguous(scales, scales.dtype, "scales")
+    if codes.dim() != 2 or scales.dim() != 2 or scales.shape[0] != codes.shape[0] or scales.shape[1] < 1:
+        raise ValueError("expected codes [N, K/2], scales [N, K/group]")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if K % scales.shape[1]:
+        raise ValueError("scales: expected [N, K/group]")
+    group = K // scales.shape[1]
+    _flat(zeros, torch.uint8, scales.numel(), "zeros")
+    n = lib().moe_q4_weight_bytes(N, K, group, 0 if zeros is None else 1)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_q4_weight_bytes")
+    data = _made(n, codes, stream)
+    _check(lib().moe_q4_prepare(_ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(data), n, _stream(stream)),
+           "moe_q4_prepare")
+    return Q4Weight(data, N, K, group, scales.dtype, zeros is not None)
+
+
+def linear_q4_workspace_bytes(M: int, N: int, K: int) -> int:
+    n = lib().moe_linear_q4_workspace_bytes(M, N, K)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_linear_q4_workspace_bytes")
+    return n
+
+
+def linear_q4(x, w: Q4Weight, ws: Workspace, bias=None, activation: str = "none", residual=None, y=None, stream=None):
+    """act(x w^T + bias) + residual with weights of 4 bits (moe_linear_q4): x [M,K], w
+    from ``q4_prepare``, the others as in ``linear``.  -> y [M,N]."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unknown activation {activation!r}")
+    if not isinstance(w, Q4Weight):
+        raise TypeError("w: expected the weights that q4_prepare gives")
+    if x.dtype is not w.dtype:
+        raise TypeError(f"x: expected the scales' type, {w.dtype}")
+    if x.dim() != 2:
+        raise ValueError("expected x [M, K]")
+    if not x.is_cuda:
+        _refuse(x, x.dtype, "x")
+    if y is None:
+        y = _made((x.shape[0], w.N), x, stream)
+    status = _binding().linear_q4(x, w.data, w.N, w.K, w.group, w.zeros, bias, act, residual, y, ws.ptr(), ws.nbytes,
+                                  _stream(stream))
+    if status == 0:
+        return y
+    if status is not None:
+        raise MoeError(status, "moe_linear_q4")
+    M = x.shape[0]
+    _rows(x, x.dtype, M, w.K, "x")
+    _rows(y, x.dtype, M, w.N, "y")
+    if residual is not None:
+        _rows(residual, x.dtype, M, w.N, "residual")
+    _flat(bias, x.dtype, w.N, "bias")
+    _contiguous(w.data, torch.uint8, "w")
+    raise _wrong("linear_q4")
 
 
 def kv4_shape(pages: int, page_size: int, Hkv: int, D: int) -> Tuple[int, int, int]:
