@@ -1,17 +1,13 @@
 // Matrix product with weights of 4 bits (moe_linear_q4): y = act(x W^T + bias) + residual,
 // W[n, k] = s[n, k / g] (c[n, k] - z[n, k / g]), c and z whole numbers 0 .. 15, s 16-bit.
 //
-// No weight is rounded: the MMA multiplies the whole numbers c - z, which both 16-bit types
-// hold exactly, and a group's fp32 sum is multiplied by its scale as it is added to the
-// output's, in fp32.
-//
-// Bound by the bytes of the weights for few rows (4096 x 4096: 8.6 MB, 1.3 us), by the
-// tensor cores for many.  In between stands the expansion: a word of 8 codes takes 11
-// instructions (9 in f16) to become the operand.  As in the attention over a 4-bit cache
-// the weights are the MMA's M side, so that a thread that holds a weight row expands it
-// into its own lane of tensor memory, and the group's scale of that row is one register
-// of the thread that adds the sums up: scales and zeros cost a multiplication a row and
-// token and none a weight, and weights pass shared memory once.
+// No weight is rounded: (c - z) s has 13 significant bits in bf16 and 16 in f16 at most, and
+// goes to the MMA as two numbers of the type, the product rounded and what the rounding
+// took off, which one fused multiply-add gives exactly.  Twice the products, but one sum a
+// row and token from the first input to the last, which stays in tensor memory (groups'
+// sums, scaled as they were added up, were bound by their reading: 650 us at 2048 x 4096 x
+// 12288 in groups of 64).  Scales are finite with 15 |s| in the type's range; an infinity
+// in x gives NaN.
 //
 // Layout (moe_q4_prepare, once a set of weights): for every 128 rows and 128 inputs one run
 // of bytes, [4][128 rows][16 bytes] of codes (32 inputs of a row in 16 bytes, inputs 2 j and
@@ -20,10 +16,10 @@
 // bytes side by side.
 //
 // A CTA (one per SM): warp 0 copies weight blocks and token tiles into a ring of stages,
-// warp 1 issues the MMAs, warpgroups 1 to 3 expand blocks in turn, warpgroup 4 adds the
-// groups' sums up and runs the epilogue.  Few tiles are shared by clusters of CTAs, each a
-// range of K, whose sums meet in distributed shared memory in rank order; of many, each CTA
-// takes its share one after the other.
+// warp 1 issues the MMAs, warpgroups 1 to 4 expand half a block each in turn, and
+// warpgroups 5 and 6 run a tile's epilogue under the next one's products.  Few tiles are shared
+// by clusters of CTAs, each a range of K, whose sums meet in distributed shared memory in
+// rank order; of many, each CTA takes its share one after the other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -35,20 +31,18 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kExpanders = 3;       // warpgroups that expand
+constexpr int kThreads = 896;
+constexpr int kExpanders = 4;       // warpgroups that expand, each with a buffer
 constexpr int kBlock = 128;         // inputs of a block
+constexpr int kHalf = kBlock / 2;   // inputs of a buffer
 constexpr int kRows = 128;          // weight rows of a tile
 constexpr int kMaxTok = 128;        // tokens of a tile
 constexpr int kSmem = 226 * 1024;
 constexpr int kQ4Stages = 14;
 constexpr int kMaxCluster = 8;
 constexpr int kCodeBytes = kRows * kBlock / 2;
-// tensor memory: the expanded blocks, then the groups' sums
-constexpr uint32_t kSumsCol = kExpanders * (kBlock / 2);
-constexpr int kSumsCols = 256, kMaxSums = 8;
-// Registers a thread, moved between the warpgroups: 56 + 3 x 64 + 224 <= 5 x 96
-constexpr int kRegsFew = 56, kRegsExpand = 64, kRegsSum = 224;
+// tensor memory: the expanded halves (products rounded, then the rest), then two tiles' sums
+constexpr uint32_t kSumsCol = kExpanders * kHalf;
 
 struct Q4Params {
   int M, N, K, k_blocks;
@@ -56,7 +50,7 @@ struct Q4Params {
   int zeros;                 // 1: the groups have zero points (else 8)
   int block_bytes;           // of a weight block
   int n_tok, row_tiles, tok_tiles;
-  int stages, cluster, sums; // sums: buffers of a group's sums in tensor memory
+  int stages, cluster;
   const uint8_t* w;
   const uint16_t *bias, *residual;
   uint16_t* y;
@@ -68,7 +62,7 @@ struct Q4Params {
 struct Control {
   uint64_t full[kQ4Stages], empty[kQ4Stages];
   uint64_t a_full[kExpanders], a_empty[kExpanders];
-  uint64_t d_full[kMaxSums], d_empty[kMaxSums], drain;
+  uint64_t d_full[2], d_empty[2], drain;
   uint32_t tmem;
   int abort_flag;
 };
@@ -86,26 +80,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
-                                       uint32_t accumulate) {
+// (of the warp that issues, one lane is `lead`)
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\ttcgen05.mma.cta_group::1."
-      "kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %3};"
+      "\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ unsigned long long pair(float a, float b) {
-  unsigned long long v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ void unpair(unsigned long long v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ uint32_t mask_or(uint32_t a, uint32_t mask, uint32_t magic) {
   uint32_t d;
@@ -145,6 +134,18 @@ __device__ __forceinline__ void expand8(uint32_t w, uint32_t off, uint32_t off16
   }
 }
 
+// v s rounded, and the rest of it.
+template <bool kBf16>
+__device__ __forceinline__ void scale2(uint32_t v, uint32_t s, uint32_t& hi, uint32_t& lo) {
+  if (kBf16) {
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(s));
+    asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}" : "=r"(lo) : "r"(v), "r"(s), "r"(hi));
+  } else {
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(s));
+    asm("{\n\t.reg .b32 n;\n\tneg.f16x2 n, %3;\n\tfma.rn.f16x2 %0, %1, %2, n;\n\t}" : "=r"(lo) : "r"(v), "r"(s), "r"(hi));
+  }
+}
+
 __device__ __forceinline__ bool warp_wait(Control& c, uint64_t* bar, uint32_t parity, int32_t* status, int32_t info) {
   const bool ok = mbar_wait(bar, parity, &c.abort_flag);
   if (__all_sync(0xffffffffu, ok)) return true;
@@ -169,6 +170,55 @@ struct Tiles {
   }
 };
 
+// The epilogue of token t's outputs [n, n + 4).
+template <bool kBf16>
+__device__ __forceinline__ void finish4(const Q4Params& p, const float4& sum, int t, int n) {
+  if (n >= p.N) return;
+  float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  ushort4 b = make_ushort4(0, 0, 0, 0), res = b, out;
+  if (p.residual) res = *reinterpret_cast<const ushort4*>(p.residual + t * p.res_stride + n);
+  if (p.bias) b = __ldg(reinterpret_cast<const ushort4*>(p.bias + n));
+  uint16_t* o = &out.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (p.bias) v[i] += to_f<kBf16>((&b.x)[i]);
+    v[i] = activate(v[i], p.act);
+    if (p.residual) v[i] += to_f<kBf16>((&res.x)[i]);
+    o[i] = from_f<kBf16>(v[i]);
+  }
+  *reinterpret_cast<ushort4*>(p.y + t * p.y_stride + n) = out;
+}
+
+template <int kAct>
+__device__ __forceinline__ void activate16(float (&v)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = activate(v[k], kAct);
+}
+// The epilogue of output n of tokens [t, t + m), m <= 16 (a warp's lanes: 32 outputs side by
+// side).
+template <bool kBf16>
+__device__ __forceinline__ void finish16(const Q4Params& p, const uint32_t (&sum)[16], float b, int t, int m, int n) {
+  uint16_t res[16] = {};
+  if (p.residual) {
+    const uint16_t* r = p.residual + t * p.res_stride + n;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k < m) res[k] = r[k * p.res_stride];
+  }
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(sum[k]) + b;
+  // (one branch for the 16)
+  if (p.act == MOE_ACT_SILU) activate16<MOE_ACT_SILU>(v);
+  else if (p.act == MOE_ACT_GELU) activate16<MOE_ACT_GELU>(v);
+  else if (p.act == MOE_ACT_GELU_TANH) activate16<MOE_ACT_GELU_TANH>(v);
+  else if (p.act == MOE_ACT_RELU) activate16<MOE_ACT_RELU>(v);
+  uint16_t* y = p.y + t * p.y_stride + n;
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (k < m) y[k * p.y_stride] = from_f<kBf16>(p.residual ? v[k] + to_f<kBf16>(res[k]) : v[k]);
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_q4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ Q4Params p) {
@@ -186,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.abort_flag = 0;
     for (int s = 0; s < p.stages; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 9); }
     for (int s = 0; s < kExpanders; ++s) { mbar_init(&c.a_full[s], 4); mbar_init(&c.a_empty[s], 1); }
-    for (int s = 0; s < p.sums; ++s) { mbar_init(&c.d_full[s], 1); mbar_init(&c.d_empty[s], 4); }
+    for (int s = 0; s < 2; ++s) { mbar_init(&c.d_full[s], 1); mbar_init(&c.d_empty[s], 8); }
     mbar_init(&c.drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_x);
@@ -208,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   bool ok = true;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
       if (elect()) {
         const uint64_t pol = l2_evict_first_policy();
@@ -240,73 +289,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      if (elect()) {
-        const uint32_t id = kBf16 ? idesc_bf16(kRows, p.n_tok) : idesc_f16(kRows, p.n_tok);
-        const int steps = 1 << (p.group_log2 - 4);  // MMAs of a group
-        Ring r, a, d;
-        for (int t = tiles.at; t < tiles.end && ok; t += tiles.step)
-          for (int kb = tiles.kb0; kb < tiles.kb1 && ok; ++kb) {
-            ok = mbar_wait(&c.full[r.stage], r.phase, &c.abort_flag) && mbar_wait(&c.a_full[a.stage], a.phase, &c.abort_flag);
-            if (!ok) { record_failure(p.status, &c.abort_flag, kInfoFull); break; }
-            const uint32_t b = kDescLoK + (smem_u32(mem + r.stage * stage_space) >> 4);
-            const uint32_t at = tmem + a.stage * (kBlock / 2);
-            for (int g = 0; g < groups; ++g) {
-              ok = mbar_wait(&c.d_empty[d.stage], d.phase ^ 1u, &c.abort_flag);
-              if (!ok) { record_failure(p.status, &c.abort_flag, kInfoAccEmpty); break; }
-              tc_fence_after();
-              const uint32_t sums = tmem + kSumsCol + d.stage * (kSumsCols / p.sums);
-#pragma unroll 2
-              for (int i = 0; i < steps; ++i) {
-                const int ks = g * steps + i;
-                mma_ts(sums, at + ks * 8, b + (ks / 4) * (x_bytes / 32) + (ks % 4) * 2, kDescHi, id, i > 0 ? 1u : 0u);
-              }
-              mma_commit(&c.d_full[d.stage]);
-              d.next(p.sums);
+      // all lanes go along, so that addresses stay uniform; one issues
+      const uint32_t lead = elect() ? 1u : 0u;
+      const uint32_t id = kBf16 ? idesc_bf16(kRows, p.n_tok) : idesc_f16(kRows, p.n_tok);
+      const uint32_t b_base = kDescLoK + (smem_u32(mem) >> 4), b_stage = stage_space >> 4, b_half = x_bytes >> 5;
+      Ring r;
+      uint32_t a_phase = 0, turn = 0, tile = 0;
+      for (int t = tiles.at; t < tiles.end && ok; t += tiles.step, ++tile) {
+        const uint32_t sums = tmem + kSumsCol + (tile & 1) * kMaxTok;
+        ok = warp_wait(c, &c.d_empty[tile & 1], (tile >> 1 & 1) ^ 1u, p.status, kInfoAccEmpty);
+        if (!ok) break;
+        uint32_t more = 0;
+        bool ready = false;
+        for (int kb = tiles.kb0; kb < tiles.kb1; ++kb) {
+          uint32_t b = b_base + r.stage * b_stage;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // (the expanders have seen the stage's copies land, the tokens' with the weights')
+            if (!ready) ok = warp_wait(c, &c.a_full[turn], a_phase, p.status, kInfoFull);
+            if (!ok) break;
+            tc_fence_after();
+            // the next buffer is asked after while these products are issued
+            const uint32_t a = tmem + turn * kHalf, a_next = turn + 1 < kExpanders ? turn + 1 : 0;
+            const uint32_t next_phase = a_next ? a_phase : a_phase ^ 1u;
+            const bool next = mbar_test_wait(&c.a_full[a_next], next_phase);
+#pragma unroll
+            for (int i = 0; i < kHalf / 16; ++i) {
+              mma_ts(sums, a + i * 8, b + i * 2, id, i ? 1u : more, lead);
+              mma_ts(sums, a + kHalf / 2 + i * 8, b + i * 2, id, 1u, lead);
             }
-            mma_commit(&c.a_empty[a.stage]);
-            mma_commit(&c.empty[r.stage]);
-            a.next(kExpanders);
-            r.next(p.stages);
+            more = 1u;
+            commit_by(&c.a_empty[turn], lead);
+            b += b_half;
+            turn = a_next;
+            a_phase = next_phase;
+            ready = __all_sync(0xffffffffu, next);
           }
-        // every MMA issued above has completed once `drain` flips
-        mma_commit(&c.drain);
-        if (!mbar_wait(&c.drain, 0, nullptr)) record_failure(p.status, &c.abort_flag, kInfoDrain);
+          if (!ok) break;
+          commit_by(&c.empty[r.stage], lead);
+          r.next(p.stages);
+        }
+        if (ok) commit_by(&c.d_full[tile & 1], lead);
       }
+      // every MMA issued above has completed once `drain` flips
+      commit_by(&c.drain, lead);
+      if (!mbar_wait(&c.drain, 0, nullptr) && lead) record_failure(p.status, &c.abort_flag, kInfoDrain);
     }
   } else if (warp < 4 + 4 * kExpanders) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
-    // a thread a row; of three warpgroups, each takes every third block
-    const int turn = warp / 4 - 1, row = tid & 127;
-    const uint32_t dst = tmem + turn * (kBlock / 2) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // a thread a row; of four warpgroups, each takes every second block's first or second half
+    const int turn = warp / 4 - 1, row = tid & 127, half = turn & 1;
+    const uint32_t dst = tmem + turn * kHalf + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     Ring r;
-    int n = 0;
+    int odd = 0;
     uint32_t phase = 1;
     for (int t = tiles.at; t < tiles.end && ok; t += tiles.step)
-      for (int kb = tiles.kb0; kb < tiles.kb1; ++kb, ++n, r.next(p.stages)) {
-        if (n % kExpanders != turn) {
-          continue;
-        }
+      for (int kb = tiles.kb0; kb < tiles.kb1; ++kb, odd ^= 1, r.next(p.stages)) {
+        if (odd != turn >> 1) continue;
         ok = warp_wait(c, &c.full[r.stage], r.phase, p.status, kInfoFull);
         if (!ok) break;
+        const uint8_t* st = mem + r.stage * stage_space + x_bytes;
+        uint4 w = *reinterpret_cast<const uint4*>(st + (half * 2 * kRows + row) * 16);
         ok = warp_wait(c, &c.a_empty[turn], phase, p.status, kInfoAccEmpty);
         if (!ok) break;
         phase ^= 1u;
         tc_fence_after();
-        const uint8_t* st = mem + r.stage * stage_space + x_bytes;
-        const uint8_t* zeros = st + kCodeBytes + groups * kRows * 2 + row;
-        uint4 w = *reinterpret_cast<const uint4*>(st + row * 16);
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-          if (q < 3) w = *reinterpret_cast<const uint4*>(st + ((q + 1) * kRows + row) * 16);
-          const uint32_t z = p.zeros ? zeros[(q * 32 >> p.group_log2) * kRows] : 8u;
+          if (q == 0) w = *reinterpret_cast<const uint4*>(st + ((half * 2 + 1) * kRows + row) * 16);
+          const int g = ((half * 2 + q) * 32 >> p.group_log2) * kRows + row;
+          uint32_t s = reinterpret_cast<const uint16_t*>(st + kCodeBytes)[g];
+          s |= s << 16;
+          const uint32_t z = p.zeros ? st[kCodeBytes + groups * kRows * 2 + g] : 8u;
           const uint32_t off = magic2<kBf16>(z);
           // -(64 + z) in f16: z counts 16 of its last bits
           const uint32_t off16 = 0xd400d400u + z * 0x00100010u;
-          uint32_t o[16];
+          uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) expand8<kBf16>(x[i], off, off16, o + 4 * i);
-          tmem_st16(dst + q * 16, o);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+            expand8<kBf16>(x[i], off, off16, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) scale2<kBf16>(v[k], s, hi[4 * i + k], lo[4 * i + k]);
+          }
+          tmem_st16(dst + q * 16, hi);
+          tmem_st16(dst + kHalf / 2 + q * 16, lo);
         }
         arrive_warp(&c.empty[r.stage]);
         tmem_st_wait();
@@ -314,78 +381,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive_warp(&c.a_full[turn]);
       }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
-    // a thread a row: its outputs of all the tile's tokens
-    const int row = tid & 127;
-    const uint32_t src = tmem + kSumsCol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    Ring r, d;
-    for (int t = tiles.at; t < tiles.end && ok; t += tiles.step) {
-      unsigned long long acc[kMaxTok / 2];
-#pragma unroll
-      for (int i = 0; i < kMaxTok / 2; ++i) acc[i] = 0ull;
-      for (int kb = tiles.kb0; kb < tiles.kb1 && ok; ++kb) {
-        ok = warp_wait(c, &c.full[r.stage], r.phase, p.status, kInfoFull);
-        if (!ok) break;
-        const uint16_t* scales =
-            reinterpret_cast<const uint16_t*>(mem + r.stage * stage_space + x_bytes + kCodeBytes) + row;
-        for (int g = 0; g < groups; ++g) {
-          const float s = to_f<kBf16>(scales[g * kRows]);
-          if (g == groups - 1) arrive_warp(&c.empty[r.stage]);
-          ok = warp_wait(c, &c.d_full[d.stage], d.phase, p.status, kInfoAccFull);
-          if (!ok) break;
-          tc_fence_after();
-          const unsigned long long s2 = pair(s, s);
-          const uint32_t at = src + d.stage * (kSumsCols / p.sums);
-#pragma unroll
-          for (int i = 0; i < kMaxTok / 16; ++i)
-            if (16 * i < p.n_tok) {
-              uint32_t v[16];
-              tmem_ld16(at + 16 * i, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                acc[8 * i + k] = fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), s2, acc[8 * i + k]);
-            }
-          tc_fence_before();
-          arrive_warp(&c.d_empty[d.stage]);
-          d.next(p.sums);
-        }
-        r.next(p.stages);
-      }
+    // a thread a row, 16 tokens at a time, of two warpgroups each takes every second 16
+    const int row = tid & 127, first = (warp / 4 - 1 - kExpanders) * 16;
+    const uint32_t lanes = tmem + kSumsCol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    uint32_t tile = 0;
+    for (int t = tiles.at; t < tiles.end && ok; t += tiles.step, ++tile) {
+      ok = warp_wait(c, &c.d_full[tile & 1], tile >> 1 & 1, p.status, kInfoAccFull);
       if (!ok) break;
-      const int n = t % p.row_tiles * kRows + row, t0 = t / p.row_tiles * p.n_tok, toks = min(p.n_tok, p.M - t0);
-      if (p.cluster == 1) {
-        if (n < p.N) {
-          const float bias = p.bias ? to_f<kBf16>(p.bias[n]) : 0.f;
-          uint16_t* y = p.y + t0 * p.y_stride + n;
-          const uint16_t* res = p.residual ? p.residual + t0 * p.res_stride + n : nullptr;
+      tc_fence_after();
+      const int t0 = t / p.row_tiles * p.n_tok, toks = min(p.n_tok, p.M - t0);
+      const uint32_t src = lanes + (tile & 1) * kMaxTok;
+      if (p.cluster > 1) {
+        // token-major over the stages (every copy and product is complete: a cluster has one tile)
+        float* part = reinterpret_cast<float*>(mem) + row;
+        for (int i = first; i < toks; i += 32) {
+          uint32_t v[16];
+          tmem_ld16(src + i, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < kMaxTok / 2; ++i)
-            if (2 * i < toks) {
-              float v[2];
-              unpair(acc[i], v[0], v[1]);
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (2 * i + e < toks) {
-                  float z = activate(v[e] + bias, p.act);
-                  if (res) z += to_f<kBf16>(res[(2 * i + e) * p.res_stride]);
-                  y[(2 * i + e) * p.y_stride] = from_f<kBf16>(z);
-                }
-            }
+          for (int k = 0; k < 16; ++k) part[(i + k) * kRows] = __uint_as_float(v[k]);
         }
       } else {
-        // this CTA's sums, token-major, over the stages: all of them have been read (the
-        // last group's sums were complete), and a cluster has one tile
-        float* part = reinterpret_cast<float*>(mem);
-#pragma unroll
-        for (int i = 0; i < kMaxTok / 2; ++i)
-          if (2 * i < toks) {
-            float v[2];
-            unpair(acc[i], v[0], v[1]);
-            part[2 * i * kRows + row] = v[0];
-            part[(2 * i + 1) * kRows + row] = v[1];
-          }
+        const int n = t % p.row_tiles * kRows + row;
+        const float b = p.bias && n < p.N ? to_f<kBf16>(p.bias[n]) : 0.f;
+        for (int i = first; i < toks; i += 32) {
+          uint32_t v[16];
+          tmem_ld16(src + i, v);
+          tmem_ld_wait();
+          if (n < p.N) finish16<kBf16>(p, v, b, t0 + i, min(16, toks - i), n);
+          __syncwarp();
+        }
       }
+      tc_fence_before();
+      arrive_warp(&c.d_empty[tile & 1]);
     }
   }
   __syncwarp();
@@ -395,26 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = tiles.at % p.row_tiles * kRows + lane * 4, t0 = tiles.at / p.row_tiles * p.n_tok;
     const int toks = min(p.n_tok, p.M - t0);
     const int ta = toks * rank / p.cluster, tb = toks * (rank + 1) / p.cluster;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.bias && n < p.N)
-      for (int i = 0; i < 4; ++i) bias[i] = to_f<kBf16>(p.bias[n + i]);
     for (int t = ta + warp; t < tb; t += kThreads / 32) {
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       const uint32_t local = smem_u32(part + t * kRows + lane * 4);
       for (int q = 0; q < p.cluster; ++q) {
         const float4 f = ld_cluster4(local, q);
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
       }
-      if (n < p.N) {
-        ushort4 out;
-        uint16_t* o = &out.x;
-        for (int i = 0; i < 4; ++i) {
-          float z = activate(v[i] + bias[i], p.act);
-          if (p.residual) z += to_f<kBf16>(p.residual[(t0 + t) * p.res_stride + n + i]);
-          o[i] = from_f<kBf16>(z);
-        }
-        *reinterpret_cast<ushort4*>(p.y + (t0 + t) * p.y_stride + n) = out;
-      }
+      finish4<kBf16>(p, v, t0 + t, n);
     }
     cluster_sync();  // the others have read this CTA's sums
   }
@@ -468,10 +484,39 @@ moe_status check_weights(int N, int K, int group) {
   return MOE_OK;
 }
 
-// CTAs that share a tile: as many as the SMs hold at once, each with 4 blocks at least.
+// How many clusters of c CTAs fit on the current device at once (0 on failure), asked once
+// a device and size, of an empty kernel of the same shape (see linear.cu).
+__global__ void __launch_bounds__(kThreads, 1) q4_shape_kernel() {}
+
+int resident_clusters(int c) {
+  static std::atomic<int> known[kMaxCluster + 1][64];
+  int d = 0;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return 0;
+  int n = known[c][d].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(q4_shape_kernel, kSmem, done) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(c * 1024);  // more than fit
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = c;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, q4_shape_kernel, &cfg) != cudaSuccess) return 0;
+  known[c][d].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs that share a tile: as many as are resident at once, each with 2 blocks at least.
 int cluster_size(int tiles, int k_blocks, int sms) {
   int c = 1;
-  while (c < kMaxCluster && (c + 1) * tiles <= sms && k_blocks / (c + 1) >= 4) ++c;
+  while (c < kMaxCluster && (c + 1) * tiles <= sms && k_blocks / (c + 1) >= 2 && resident_clusters(c + 1) >= tiles) ++c;
   return c;
 }
 
@@ -584,7 +629,6 @@ moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const 
   p.cluster = cluster_size(static_cast<int>(tiles < sms ? tiles : sms), p.k_blocks, sms);
   p.stages = (kSmem - 1024) / (p.n_tok * kBlock * 2 + ceil_div(p.block_bytes, 1024) * 1024);
   if (p.stages > kQ4Stages) p.stages = kQ4Stages;
-  p.sums = kSumsCols / (p.n_tok <= 32 ? 32 : p.n_tok <= 64 ? 64 : 128);
   p.w = static_cast<const uint8_t*>(weights);
   p.bias = static_cast<const uint16_t*>(bias);
   p.residual = static_cast<const uint16_t*>(residual); p.res_stride = residual_stride;
