@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build", platform.machine())
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["route.cu", "gemm.cu", "slice.cu", "mx.cu", "api.cu", "noalloc.cu", "qk_norm_rope.cu",
-           "prefix_attention.cu", "linear.cu", "linear_q4.cu", "kv4.cu", "pages.cu",
+           "prefix_attention.cu", "linear.cu", "linear_q4.cu", "linear_q4_few.cu", "kv4.cu", "pages.cu",
            "attention_kv4.cu", "attention_kv4_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

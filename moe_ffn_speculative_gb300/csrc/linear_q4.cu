@@ -9,12 +9,6 @@
 // 12288 in groups of 64).  Scales are finite with 15 |s| in the type's range; an infinity
 // in x gives NaN.
 //
-// Layout (moe_q4_prepare, once a set of weights): for every 128 rows and 128 inputs one run
-// of bytes, [4][128 rows][16 bytes] of codes (32 inputs of a row in 16 bytes, inputs 2 j and
-// 2 j + 1 of every 8 in nibbles j and j + 4, where one mask finds both), then the groups'
-// scales [128 / g][128 rows] and zeros.  A block is one copy, and a warp's lanes read 512
-// bytes side by side.
-//
 // A CTA (one per SM): warp 0 copies weight blocks and token tiles into a ring of stages,
 // warp 1 issues the MMAs, warpgroups 1 to 4 expand half a block each in turn, and
 // warpgroups 5 and 6 run a tile's epilogue under the next one's products.  Few tiles are shared
@@ -25,6 +19,7 @@
 #include <string.h>
 
 #include "epilogue.cuh"
+#include "linear_q4.cuh"
 #include "moe.h"
 #include "moe_internal.cuh"
 
@@ -33,31 +28,13 @@ namespace {
 
 constexpr int kThreads = 896;
 constexpr int kExpanders = 4;       // warpgroups that expand, each with a buffer
-constexpr int kBlock = 128;         // inputs of a block
 constexpr int kHalf = kBlock / 2;   // inputs of a buffer
-constexpr int kRows = 128;          // weight rows of a tile
 constexpr int kMaxTok = 128;        // tokens of a tile
 constexpr int kSmem = 226 * 1024;
 constexpr int kQ4Stages = 14;
 constexpr int kMaxCluster = 8;
-constexpr int kCodeBytes = kRows * kBlock / 2;
 // tensor memory: the expanded halves (products rounded, then the rest), then two tiles' sums
 constexpr uint32_t kSumsCol = kExpanders * kHalf;
-
-struct Q4Params {
-  int M, N, K, k_blocks;
-  int group, group_log2;     // inputs of a group: 32, 64 or 128
-  int zeros;                 // 1: the groups have zero points (else 8)
-  int block_bytes;           // of a weight block
-  int n_tok, row_tiles, tok_tiles;
-  int stages, cluster;
-  const uint8_t* w;
-  const uint16_t *bias, *residual;
-  uint16_t* y;
-  long long res_stride, y_stride;
-  int act;
-  int32_t* status;
-};
 
 struct Control {
   uint64_t full[kQ4Stages], empty[kQ4Stages];
@@ -66,10 +43,6 @@ struct Control {
   uint32_t tmem;
   int abort_flag;
 };
-
-__host__ __device__ constexpr int block_bytes(int group, bool zeros) {
-  return kCodeBytes + kBlock / group * kRows * (zeros ? 3 : 2);
-}
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -96,44 +69,6 @@ __device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ uint32_t mask_or(uint32_t a, uint32_t mask, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(mask), "r"(magic));
-  return d;
-}
-// A type's numbers 2^e + z, in both halves: what is taken off a code that has been put
-// into the mantissa of 2^e (bf16: 128; f16: 1024).
-template <bool kBf16>
-__device__ __forceinline__ uint32_t magic2(uint32_t z) {
-  return (kBf16 ? 0x43004300u : 0x64006400u) + z * 0x00010001u;
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if (kBf16) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// 8 codes as whole numbers less z (off = magic2(z)), pairs of neighbouring inputs.  In f16
-// a code may stay in the mantissa's next four bits, where it counts 16: 1024 + 16 c, of
-// which a sixteenth less 64 + z (off16, negative) is exact too.
-template <bool kBf16>
-__device__ __forceinline__ void expand8(uint32_t w, uint32_t off, uint32_t off16, uint32_t* o) {
-  if (kBf16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = sub2<true>(mask_or(w >> (4 * j), 0x000f000fu, 0x43004300u), off);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t v = w >> (8 * j);
-      o[2 * j] = sub2<false>(mask_or(v, 0x000f000fu, 0x64006400u), off);
-      asm("fma.rn.f16x2 %0, %1, %2, %3;"
-          : "=r"(o[2 * j + 1])
-          : "r"(mask_or(v, 0x00f000f0u, 0x64006400u)), "r"(0x2c002c00u), "r"(off16));
-    }
-  }
-}
-
 // v s rounded, and the rest of it.
 template <bool kBf16>
 __device__ __forceinline__ void scale2(uint32_t v, uint32_t s, uint32_t& hi, uint32_t& lo) {
@@ -620,6 +555,14 @@ moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const 
   p.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
   p.zeros = has_zeros;
   p.block_bytes = block_bytes(group, has_zeros != 0);
+  p.w = static_cast<const uint8_t*>(weights);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual); p.res_stride = residual_stride;
+  p.y = static_cast<uint16_t*>(y); p.y_stride = y_stride;
+  p.act = activation;
+  p.status = static_cast<int32_t*>(ws);
+  const bool f16 = dtype == MOE_DTYPE_F16;
+  if (M <= kQ4FewRows) return launch_linear_q4_few(f16, p, x, x_stride, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   p.row_tiles = ceil_div(N, kRows);
   p.tok_tiles = ceil_div(M, kMaxTok);
   p.n_tok = ceil_div(ceil_div(M, p.tok_tiles), 16) * 16;
@@ -629,13 +572,6 @@ moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const 
   p.cluster = cluster_size(static_cast<int>(tiles < sms ? tiles : sms), p.k_blocks, sms);
   p.stages = (kSmem - 1024) / (p.n_tok * kBlock * 2 + ceil_div(p.block_bytes, 1024) * 1024);
   if (p.stages > kQ4Stages) p.stages = kQ4Stages;
-  p.w = static_cast<const uint8_t*>(weights);
-  p.bias = static_cast<const uint16_t*>(bias);
-  p.residual = static_cast<const uint16_t*>(residual); p.res_stride = residual_stride;
-  p.y = static_cast<uint16_t*>(y); p.y_stride = y_stride;
-  p.act = activation;
-  p.status = static_cast<int32_t*>(ws);
-  const bool f16 = dtype == MOE_DTYPE_F16;
   CUtensorMap tm_x;
   const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};
   const uint64_t xst[1] = {static_cast<uint64_t>(M > 1 ? x_stride : K) * 2};
