@@ -105,23 +105,18 @@ struct Tiles {
   }
 };
 
-// The epilogue of token t's outputs [n, n + 4).
+// The epilogue of a token's outputs [n, n + 4).
 template <bool kBf16>
-__device__ __forceinline__ void finish4(const Q4Params& p, const float4& sum, int t, int n) {
-  if (n >= p.N) return;
+__device__ __forceinline__ void finish4(const Q4Params& p, const float4& sum, const ushort4& b, const ushort4& res, uint16_t* y) {
   float v[4] = {sum.x, sum.y, sum.z, sum.w};
-  ushort4 b = make_ushort4(0, 0, 0, 0), res = b, out;
-  if (p.residual) res = *reinterpret_cast<const ushort4*>(p.residual + t * p.res_stride + n);
-  if (p.bias) b = __ldg(reinterpret_cast<const ushort4*>(p.bias + n));
+  ushort4 out;
   uint16_t* o = &out.x;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (p.bias) v[i] += to_f<kBf16>((&b.x)[i]);
-    v[i] = activate(v[i], p.act);
-    if (p.residual) v[i] += to_f<kBf16>((&res.x)[i]);
-    o[i] = from_f<kBf16>(v[i]);
+    v[i] = activate(v[i] + to_f<kBf16>((&b.x)[i]), p.act);
+    o[i] = from_f<kBf16>(p.residual ? v[i] + to_f<kBf16>((&res.x)[i]) : v[i]);
   }
-  *reinterpret_cast<ushort4*>(p.y + t * p.y_stride + n) = out;
+  *reinterpret_cast<ushort4*>(y) = out;
 }
 
 template <int kAct>
@@ -353,21 +348,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (p.cluster > 1) {
-    cluster_sync();
-    const float* part = reinterpret_cast<const float*>(mem);
+    // this CTA's share of the tokens, a warp a token and a lane 4 outputs; what the epilogue
+    // reads comes while the others finish
+    constexpr int kWarps = kThreads / 32, kEach = (kMaxTok / 2 + kWarps - 1) / kWarps;
     const int n = tiles.at % p.row_tiles * kRows + lane * 4, t0 = tiles.at / p.row_tiles * p.n_tok;
     const int toks = min(p.n_tok, p.M - t0);
-    const int ta = toks * rank / p.cluster, tb = toks * (rank + 1) / p.cluster;
-    for (int t = ta + warp; t < tb; t += kThreads / 32) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const uint32_t local = smem_u32(part + t * kRows + lane * 4);
-      for (int q = 0; q < p.cluster; ++q) {
-        const float4 f = ld_cluster4(local, q);
-        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
-      }
-      finish4<kBf16>(p, v, t0 + t, n);
+    const int ta = toks * rank / p.cluster + warp, tb = toks * (rank + 1) / p.cluster;
+    ushort4 b = make_ushort4(0, 0, 0, 0), res[kEach];
+    if (p.bias && n < p.N) b = __ldg(reinterpret_cast<const ushort4*>(p.bias + n));
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = ta + i * kWarps;
+      res[i] = make_ushort4(0, 0, 0, 0);
+      if (p.residual && n < p.N && t < tb) res[i] = *reinterpret_cast<const ushort4*>(p.residual + (t0 + t) * p.res_stride + n);
     }
-    cluster_sync();  // the others have read this CTA's sums
+    cluster_sync();
+    const uint32_t part = smem_u32(mem) + (ta * kRows + lane * 4) * 4;
+    float4 v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < p.cluster; ++q)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (ta + i * kWarps < tb) {
+          const float4 f = ld_cluster4(part + i * kWarps * kRows * 4, q);
+          v[i].x += f.x; v[i].y += f.y; v[i].z += f.z; v[i].w += f.w;
+        }
+    cluster_arrive();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int t = ta + i * kWarps;
+      if (t < tb && n < p.N) finish4<kBf16>(p, v[i], b, res[i], p.y + (t0 + t) * p.y_stride + n);
+    }
+    cluster_wait();  // the others have read this CTA's sums
   }
   // (y may be what a fused forward loads before it waits: see linear.cu)
   __threadfence();
