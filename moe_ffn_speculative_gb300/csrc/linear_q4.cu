@@ -19,6 +19,7 @@
 #include <string.h>
 
 #include "epilogue.cuh"
+#include "issue.cuh"
 #include "linear_q4.cuh"
 #include "moe.h"
 #include "moe_internal.cuh"
@@ -44,31 +45,6 @@ struct Control {
   int abort_flag;
 };
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// (of the warp that issues, one lane is `lead`)
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %3};"
-      "\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void commit_by(uint64_t* bar, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(lead)
-      : "memory");
-}
 // v s rounded, and the rest of it.
 template <bool kBf16>
 __device__ __forceinline__ void scale2(uint32_t v, uint32_t s, uint32_t& hi, uint32_t& lo) {
@@ -245,24 +221,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool next = mbar_test_wait(&c.a_full[a_next], next_phase);
 #pragma unroll
             for (int i = 0; i < kHalf / 16; ++i) {
-              mma_ts(sums, a + i * 8, b + i * 2, id, i ? 1u : more, lead);
-              mma_ts(sums, a + kHalf / 2 + i * 8, b + i * 2, id, 1u, lead);
+              mma_ts_by(lead, sums, a + i * 8, b + i * 2, id, i ? 1u : more);
+              mma_ts_by(lead, sums, a + kHalf / 2 + i * 8, b + i * 2, id, 1u);
             }
             more = 1u;
-            commit_by(&c.a_empty[turn], lead);
+            mma_commit_by(lead, &c.a_empty[turn]);
             b += b_half;
             turn = a_next;
             a_phase = next_phase;
             ready = __all_sync(0xffffffffu, next);
           }
           if (!ok) break;
-          commit_by(&c.empty[r.stage], lead);
+          mma_commit_by(lead, &c.empty[r.stage]);
           r.next(p.stages);
         }
-        if (ok) commit_by(&c.d_full[tile & 1], lead);
+        if (ok) mma_commit_by(lead, &c.d_full[tile & 1]);
       }
       // every MMA issued above has completed once `drain` flips
-      commit_by(&c.drain, lead);
+      mma_commit_by(lead, &c.drain);
       if (!mbar_wait(&c.drain, 0, nullptr) && lead) record_failure(p.status, &c.abort_flag, kInfoDrain);
     }
   } else if (warp < 4 + 4 * kExpanders) {
