@@ -7,9 +7,11 @@ in the order of use.
 
 Everything a step varies (positions, cache slots, block starts, lengths, page
 tables) stays on the device, so one captured graph serves every later step of
-the same token count.  ``python -m moe_ffn_speculative_gb300.decoder`` runs the
+the same token count.  ``DecoderLayer4`` is the layer with projections of 4 bits
+over a cache of 4 bits, and ``PagedRequests`` the pages that requests hold of such
+caches or of 16-bit ones.  ``python -m moe_ffn_speculative_gb300.decoder`` runs the
 Qwen3-8B DSpark draft layer on 8 requests x 9 tokens over a shared prefix of
-4096 tokens and prints the time of a step.
+4096 tokens, in 16 and in 4 bits, and prints the time of a step.
 """
 from __future__ import annotations
 
@@ -41,6 +43,13 @@ class KVCache:
         shape = (pages, page_size, a.kv_heads, a.head_dim)
         self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
         self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+
+
+class KVCache4:
+    """The same in 4 bits (e2m1 codes with a scale per 32 channels), a quarter of the bytes."""
+
+    def __init__(self, pages: int, page_size: int, a: AttentionConfig, device="cuda"):
+        self.data = torch.zeros(ops.kv4_shape(pages, page_size, a.kv_heads, a.head_dim), dtype=torch.uint8, device=device)
 
 
 @dataclass
@@ -105,6 +114,82 @@ class DecoderLayer:
         return h + self.ffn.forward(rms_norm(h, self.w["norm2"], self.a.eps))
 
 
+def quantize_q4(w: torch.Tensor, group: int = 128):
+    """Weights [N, K] as ``ops.q4_prepare`` takes them, (codes, scales, zeros): the
+    nearest of 16 evenly spaced values, 0 among them, from a group's least to its
+    greatest weight."""
+    f = w.float().unflatten(1, (-1, group))
+    lo, hi = f.amin(-1).clamp(max=0), f.amax(-1).clamp(min=0)
+    scales = ((hi - lo) / 15).clamp(min=2.0 ** -20).to(w.dtype)
+    s = scales.float()
+    zeros = (-lo / s).round().clamp(0, 15)
+    code = (f / s[..., None] + zeros[..., None]).round().clamp(0, 15).to(torch.uint8).flatten(1)
+    return code[:, 0::2] | code[:, 1::2] << 4, scales, zeros.to(torch.uint8)
+
+
+class DecoderLayer4(DecoderLayer):
+    """The layer with its projections in 4 bits, over a cache in 4 bits (KVCache4)."""
+
+    def __init__(self, a: AttentionConfig, weights: dict, ffn: ops.MoELayer, max_requests: int, group: int = 128):
+        super().__init__(a, weights, ffn, max_requests)
+        self.w_qkv, self.w_out = (ops.q4_prepare(*quantize_q4(weights[n], group)) for n in ("w_qkv", "w_out"))
+        T = ffn.max_tokens
+        self.ws = ops.Workspace(max(
+            ops.prefix_attention_kv4_workspace_bytes(T, max_requests, a.q_heads, a.kv_heads, a.head_dim),
+            *(ops.linear_q4_workspace_bytes(T, w.N, w.K) for w in (self.w_qkv, self.w_out))), weights["w_qkv"].device)
+
+    def attention(self, x: torch.Tensor, cache: KVCache4, b: Batch) -> torch.Tensor:
+        a, w = self.a, self.w
+        qkv = ops.linear_q4(rms_norm(x, w["norm1"], a.eps), self.w_qkv, self.ws)
+        q, k, v = (t.unflatten(1, (-1, a.head_dim))
+                   for t in qkv.split([n * a.head_dim for n in (a.q_heads, a.kv_heads, a.kv_heads)], dim=1))
+        q, k, _ = ops.qk_norm_rope(q, k, None, b.positions, self.rope, self.ws, q_weight=w["q_norm"], k_weight=w["k_norm"],
+                                   eps=a.eps)
+        ops.kv4_write(k, v, b.slots, cache.data, self.ws)
+        o = ops.prefix_attention_kv4(q, cache.data, b.q_start, b.prefix_pages, b.prefix_len, b.page_table, b.own_len,
+                                     self.ws, causal=a.causal)
+        return ops.linear_q4(o.flatten(1), self.w_out, self.ws, residual=x)
+
+
+class PagedRequests:
+    """The pages that requests hold of one layer's caches or of several layers': page
+    counts, table and lengths on the device, so that a captured step (``block``, the
+    layers, ``keep``) serves every later one.  The first `prefix_pages` pages are the
+    shared prefix's and stay taken."""
+
+    def __init__(self, requests: int, width: int, pages: int, page_size: int, caches, prefix_pages: int = 0, device="cuda"):
+        def i32(*shape, value=0):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+        self.page, self.caches = page_size, tuple(caches)
+        self.refs, self.table, self.own_len = i32(pages), i32(requests, width, value=-1), i32(requests)
+        self.refs[:prefix_pages] = 1
+        self.prefix_pages = torch.arange(prefix_pages, dtype=torch.int32, device=device) if prefix_pages else None
+        self.ws = ops.Workspace(ops.pages_workspace_bytes(requests, pages), device)
+
+    def resize(self, new_len: torch.Tensor) -> None:
+        ops.pages_resize(self.refs, self.table, self.own_len, new_len, self.page, self.ws, self.caches)
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
+        """Requests dst become copies of requests src."""
+        ops.pages_fork(self.refs, self.table, self.own_len, src, dst, self.page, self.ws, self.caches)
+
+    def block(self, n: int, prefix_len: Optional[torch.Tensor] = None):
+        """Pages for n more tokens of every request.  -> (Batch of them, the lengths before)."""
+        base = self.own_len.clone()
+        self.resize(base + n)
+        at = base[:, None] + torch.arange(n, dtype=torch.int32, device=base.device)
+        pages = self.table.gather(1, (at // self.page).clamp(max=self.table.shape[1] - 1).long())
+        positions = at if prefix_len is None else at + prefix_len
+        return Batch(positions=positions.flatten(), slots=(pages * self.page + at % self.page).flatten(),
+                     q_start=torch.arange(len(base) + 1, dtype=torch.int32, device=base.device) * n, own_len=self.own_len,
+                     page_table=self.table, prefix_pages=self.prefix_pages, prefix_len=prefix_len), base
+
+    def keep(self, base: torch.Tensor, kept: torch.Tensor) -> None:
+        """Of a block's tokens those at offsets kept [requests, n] stay (growing, the
+        first negative one ends a row), moved up behind the first `base` ones."""
+        self.resize(ops.pages_compact(self.table, base, kept, self.page, self.ws, self.caches))
+
+
 def shared_prefix_batch(requests: int, block: int, prefix: int, own: int, page: int, device="cuda") -> Batch:
     """A step of `requests` requests: `block` tokens each after `own` cached
     ones of their own and a shared prefix, pages in order."""
@@ -149,5 +234,50 @@ def main(requests: int = 8, block: int = 9, prefix: int = 4096, own: int = 500, 
     return us
 
 
+def main4(requests: int = 8, block: int = 9, prefix: int = 4096, own: int = 500, page: int = 64, steps: int = 200) -> float:
+    """Steps of the layer in 4 bits with their pages: a block of every request, of
+    which a path of three tokens stays."""
+    cfg = S.CONFIGS["qwen3_8b_dspark"].with_(T=requests * block)
+    a = AttentionConfig()
+    d = S.make_inputs(cfg, "cuda")
+    layer = DecoderLayer4(a, make_attention_weights(cfg.H, a), ops.MoELayer(d, ops.Recipe.from_config(cfg), cfg.T), requests)
+    path = [i for i in (0, 2, 3) if i < block]
+    warm = 20
+    shared, width = -(-prefix // page), -(-(own + len(path) * (steps + warm + 2) + block) // page)
+    cache = KVCache4(shared + requests * width, page, a)
+    r = PagedRequests(requests, width, cache.data.shape[0], page, [cache.data], shared)
+    heads = torch.randn((2, r.refs.numel() * page, a.kv_heads, a.head_dim), device="cuda", dtype=torch.bfloat16)
+    ops.kv4_write(heads[0], heads[1], None, cache.data, layer.ws)
+    r.resize(torch.full_like(r.own_len, own))
+    prefix_len = torch.tensor([prefix], dtype=torch.int32, device="cuda") if prefix else None
+    kept = torch.tensor([path] * requests, dtype=torch.int32, device="cuda")
+    x = d["x"]
+
+    def step():
+        b, base = r.block(block, prefix_len)
+        y = layer.forward(x, cache, b)
+        r.keep(base, kept)
+        return y
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(warm):
+        graph.replay()
+    t0, t1 = torch.cuda.Event(True), torch.cuda.Event(True)
+    t0.record()
+    for _ in range(steps):
+        graph.replay()
+    t1.record()
+    torch.cuda.synchronize()
+    for ws in (layer.ws, layer.ffn.ws, r.ws):
+        assert ws.device_status()[0] == ops.MOE_OK
+    assert r.own_len.tolist() == [own + len(path) * (1 + warm + steps)] * requests
+    us = t0.elapsed_time(t1) * 1e3 / steps
+    print(f"the same in 4 bits, with its pages: {us:.1f} us a step")
+    return us
+
+
 if __name__ == "__main__":
     main()
+    main4()
