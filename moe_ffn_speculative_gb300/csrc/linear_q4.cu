@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 896;
 constexpr int kExpanders = 4;       // warpgroups that expand, each with a buffer
+constexpr uint32_t kNegateA = 1u << 13;  // of an instruction descriptor
 constexpr int kHalf = kBlock / 2;   // inputs of a buffer
 constexpr int kMaxTok = 128;        // tokens of a tile
 constexpr int kSmem = 226 * 1024;
@@ -45,15 +46,20 @@ struct Control {
   int abort_flag;
 };
 
-// v s rounded, and the rest of it.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// v s rounded, and what that is too much (minus = -s).
 template <bool kBf16>
-__device__ __forceinline__ void scale2(uint32_t v, uint32_t s, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void scale2(uint32_t v, uint32_t s, uint32_t minus, uint32_t& hi, uint32_t& over) {
   if (kBf16) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(s));
-    asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}" : "=r"(lo) : "r"(v), "r"(s), "r"(hi));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(over) : "r"(v), "r"(minus), "r"(hi));
   } else {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(v), "r"(s));
-    asm("{\n\t.reg .b32 n;\n\tneg.f16x2 n, %3;\n\tfma.rn.f16x2 %0, %1, %2, n;\n\t}" : "=r"(lo) : "r"(v), "r"(s), "r"(hi));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(over) : "r"(v), "r"(minus), "r"(hi));
   }
 }
 
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kHalf / 16; ++i) {
               mma_ts_by(lead, sums, a + i * 8, b + i * 2, id, i ? 1u : more);
-              mma_ts_by(lead, sums, a + kHalf / 2 + i * 8, b + i * 2, id, 1u);
+              mma_ts_by(lead, sums, a + kHalf / 2 + i * 8, b + i * 2, id | kNegateA, 1u);
             }
             more = 1u;
             mma_commit_by(lead, &c.a_empty[turn]);
@@ -259,27 +265,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         phase ^= 1u;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
           if (q == 0) w = *reinterpret_cast<const uint4*>(st + ((half * 2 + 1) * kRows + row) * 16);
           const int g = ((half * 2 + q) * 32 >> p.group_log2) * kRows + row;
           uint32_t s = reinterpret_cast<const uint16_t*>(st + kCodeBytes)[g];
           s |= s << 16;
+          const uint32_t minus = s ^ 0x80008000u;
           const uint32_t z = p.zeros ? st[kCodeBytes + groups * kRows * 2 + g] : 8u;
           const uint32_t off = magic2<kBf16>(z);
           // -(64 + z) in f16: z counts 16 of its last bits
           const uint32_t off16 = 0xd400d400u + z * 0x00100010u;
-          uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
-            expand8<kBf16>(x[i], off, off16, v);
+          for (int i = 0; i < 4; i += 2) {
+            uint32_t hi[8], over[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) scale2<kBf16>(v[k], s, hi[4 * i + k], lo[4 * i + k]);
+            for (int e = 0; e < 2; ++e) {
+              uint32_t v[4];
+              expand8<kBf16>(x[i + e], off, off16, v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) scale2<kBf16>(v[k], s, minus, hi[4 * e + k], over[4 * e + k]);
+            }
+            tmem_st8(dst + q * 16 + i * 4, hi);
+            tmem_st8(dst + kHalf / 2 + q * 16 + i * 4, over);
           }
-          tmem_st16(dst + q * 16, hi);
-          tmem_st16(dst + kHalf / 2 + q * 16, lo);
         }
         arrive_warp(&c.empty[r.stage]);
         tmem_st_wait();
