@@ -610,7 +610,9 @@ MOE_API moe_status moe_q4_prepare(const uint8_t* codes, const void* scales, cons
                                   void* weights, size_t weight_bytes, cudaStream_t stream);
 
 /* moe_linear() with such weights: y_m = act(x_m W^T + bias) + residual_m, the weights as
- * they are (none is rounded), fp32 sums, one rounding.
+ * they are (none is rounded), fp32 sums, one rounding.  The weights have to be in the
+ * type's range (f16: |scale| <= 4096 will do); a row of x with an infinity gives values
+ * that are not finite.
  *   weights    from moe_q4_prepare() with this N, K, group and (has_zeros) zeros or none,
  *              and scales of this dtype
  *   ws         >= moe_linear_q4_workspace_bytes(M, N, K) bytes

@@ -11,6 +11,9 @@
 // A CTA takes 32 weight rows, its 16 warps a block of 128 inputs each in turn, 16 rows a
 // fragment; the warps' sums meet in shared memory in the warps' order.  (Fewer rows a warp
 // would read the tokens' inputs more often, more would leave SMs without work at 4096 rows.)
+//
+// Measured: 1 row of 4096 x 4096 6.2 us (floor 1.3: launch, two dependent trips to memory and
+// the joining), 4096 x 24576 20.7 us (2.6 TB/s), 16 rows 30.8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>

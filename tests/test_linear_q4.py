@@ -269,3 +269,35 @@ def test_wrong_tensors():
         ops.q4_prepare(c.codes, c.scales[:, :3].contiguous())
     empty = ops.linear_q4(c.x[:0], c.w, c.ws)
     assert empty.shape == (0, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 24, 25, 40])
+@pytest.mark.parametrize("dtype,low,high,x", [(HF, 2.0 ** -24, 40, 256.0), (HF, 2.0 ** -14, 1, 1.0), (HF, 4096.0, 1, 2.0 ** -12),
+                                              (BF, 2.0 ** -100, 1, 1.0), (BF, 2.0 ** 100, 1, 1.0)])
+def test_scales_at_the_ends_of_the_range(M, dtype, low, high, x):
+    """Subnormal, smallest and largest scales; the tolerance of the other tests (f16 outputs
+    may be subnormal: half of 2^-24)."""
+    c = Case(M, 256, 136, 32, dtype=dtype, seed=M)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    odd = torch.randint(1, 1 + high, c.scales.shape, generator=g, device="cuda") if high > 1 else 1 - torch.rand(
+        c.scales.shape, generator=g, device="cuda") * 0.49
+    c.scales = (odd.float() * low * (1 - 2 * (torch.rand(c.scales.shape, generator=g, device="cuda") < 0.5).float())).to(dtype)
+    c.x = (c.x.float() * x).to(dtype)
+    c.w = ops.q4_prepare(c.codes, c.scales, c.zeros)
+    assert bool((c.scales != 0).all())
+    c.check()
+
+
+@pytest.mark.gpu
+def test_both_kernels_agree_on_integers():
+    """Scales of 1 and whole inputs: every sum is exact, whatever kernel takes it."""
+    c = Case(40, 512, 264, 64, dtype=BF, seed=1)
+    c.scales, c.x = torch.ones_like(c.scales), c.x.mul(2).round().clamp(-3, 3)
+    c.w = ops.q4_prepare(c.codes, c.scales, c.zeros)
+    whole = c.check()
+    want = c.exact()[0]
+    assert torch.equal(whole, want.to(BF))
+    for a in range(0, 40, 10):
+        part = ops.linear_q4(c.x[a:a + 10], c.w, c.ws)
+        assert torch.equal(part, whole[a:a + 10])
