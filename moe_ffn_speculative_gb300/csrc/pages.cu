@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kBookThreads = 1024;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyChunk = kCopyThreads * 4 * 16;  // bytes a CTA copies at a time
+constexpr int kCopyChunk = kCopyThreads * 8 * 16;  // bytes a CTA copies at a time
 constexpr int kCompactThreads = 128;
 
 struct BookParams {
@@ -37,6 +37,7 @@ struct BookParams {
   const int32_t* new_len;      // resize
   const int32_t *src, *dst;    // fork
   int n;                       // fork: pairs
+  int signal;                  // the next launch is pages_copy_kernel, which waits for this one's end
   int32_t* status;
   // workspace
   int32_t* count;              // copies
@@ -137,6 +138,7 @@ enum : int { kSkip = -1, kPlain = 0, kSplit = 1 };
 
 __global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid_constant__ BookParams p) {
   __shared__ int n_copies;
+  if (p.signal) griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.B), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid
 
 __global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_constant__ BookParams p) {
   __shared__ int n_copies;
+  if (p.signal) griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.n), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
@@ -296,7 +299,9 @@ __global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_c
   if (tid == 0) *p.count = n_copies;
 }
 
-// The listed pages' bytes in every pool, a chunk a CTA at a time.
+// The listed pages' bytes in every pool, a chunk a CTA at a time.  128 requests forked (330
+// MB read and written): 69.7 us with the bookkeeping, 4.7 TB/s; with four loads a thread
+// under way instead of eight 73.6, without the streaming hints 70.8.
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
   griddep_wait();
   const int per = p.chunk0[p.n_pools];
@@ -310,16 +315,16 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
     const uint8_t* src = p.pool[k].data + c.x * bytes + at;
     uint8_t* dst = p.pool[k].data + c.y * bytes + at;
     const int left = static_cast<int>(min(static_cast<long long>(kCopyChunk), bytes - at));
-    uint4 v[4];
+    uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int o = (i * kCopyThreads + threadIdx.x) * 16;
-      if (o < left) v[i] = *reinterpret_cast<const uint4*>(src + o);
+      if (o < left) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + o));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int o = (i * kCopyThreads + threadIdx.x) * 16;
-      if (o < left) *reinterpret_cast<uint4*>(dst + o) = v[i];
+      if (o < left) __stcs(reinterpret_cast<uint4*>(dst + o), v[i]);
     }
   }
 }
@@ -507,6 +512,7 @@ moe_status run_book(void (*kernel)(BookParams), BookParams& b, const moe_page_po
   b.list = reinterpret_cast<int32_t*>(w + L.o_list);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
+  b.signal = n_pools > 0;
   if (launch(kernel, b, dim3(1), kBookThreads, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (n_pools == 0) return MOE_OK;
   c.n_pools = n_pools;
