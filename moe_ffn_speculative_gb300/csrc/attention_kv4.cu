@@ -58,13 +58,14 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 896;
+constexpr int kSoftGroups = 4;   // of the softmax, four warps each
 constexpr int kSmem = 232448;    // 227 KB
 constexpr int kMaxStages = 12;
 constexpr int kSegments = 4;
 constexpr int kReaders = kThreads / 32 - 1;  // of a segment: every warp but the one that walks
-// Registers a thread, moved between the warpgroups: 72 + 72 + 2 x 128 + 72 <= 5 x 96
-constexpr int kRegsFew = 72, kRegsSoftmax = 128;
+// Registers a thread, moved between the warpgroups: 3 x 56 + 4 x 80 <= 7 x 72
+constexpr int kRegsFew = 56, kRegsSoftmax = 80;
 
 // ---------------------------------------------------------------- tensor memory, MMA
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -373,20 +374,20 @@ __device__ __forceinline__ void drain_mma(const Kv4Attn& p, Control& c, int whic
 // us for 64 rows.)
 template <bool kBf16, int D>
 __device__ __forceinline__ void load_queries(const Kv4Attn& p, Control& c, uint8_t* q_mem, const Segment& s, int seg) {
-  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = kRows / (8 * kAtOnce);
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kWarps = 4 * kSoftGroups, kPasses = kRows / (kWarps * kAtOnce);
   const int lane = threadIdx.x & 31, ch = lane % kLanes, buf = seg & 1, rows = s.toks * p.G;
-  const int r0 = ((threadIdx.x >> 5) & 7) * kAtOnce + lane / kLanes;
+  const int r0 = ((threadIdx.x >> 5) - 8) * kAtOnce + lane / kLanes;
   uint4 x[kPasses];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int r = r0 + k * 8 * kAtOnce;
+    const int r = r0 + k * kWarps * kAtOnce;
     x[k] = make_uint4(0, 0, 0, 0);
     if (r < rows)
       x[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (s.tok0 + r / p.G) * p.q_stride + (s.h * p.G + r % p.G) * D + ch * 8));
   }
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int r = r0 + k * 8 * kAtOnce;
+    const int r = r0 + k * kWarps * kAtOnce;
     float scale = p.scale_log2;
     if (kBf16) {
       uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, top = 0;
@@ -601,9 +602,8 @@ struct Softmax {
     softmax_sync(group);
     bool ok = warp_wait(c, &c.q_full, seg & 1, p.status, kInfoAttnQuery);
     int j = s.j0;
-    if (kMine <= 16)
-      for (; j + 1 < s.j1; j += 2, i += 2)
-        if (!step<kMine, 2>(s, seg, i, j, l, ok)) return false;
+    for (; j + 1 < s.j1; j += 2, i += 2)
+      if (!step<kMine, 2>(s, seg, i, j, l, ok)) return false;
     for (; j < s.j1; ++j, ++i)
       if (!step<kMine, 1>(s, seg, i, j, l, ok)) return false;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
@@ -635,6 +635,22 @@ struct Softmax {
     softmax_sync(group);  // c.top and c.m have been read
     return true;
   }
+  // A group whose rows a segment does not have goes along with the others.
+  __device__ __forceinline__ bool without_rows(const Segment& s, int seg, int& i) {
+    bool ok = warp_wait(c, &c.q_full, seg & 1, p.status, kInfoAttnQuery);
+    for (int j = s.j0; j < s.j1 && ok; ++j, ++i) {
+      const int buf = i & 1;
+      const uint32_t phase = (i >> 1) & 1;
+      ok = warp_wait(c, &c.s_full[buf], phase, p.status, kInfoAttnScores);
+      arrive_warp(&c.s_empty[buf]);
+      ok = ok && warp_wait(c, &c.p_empty[buf], phase ^ 1u, p.status, kInfoAttnProbs);
+      arrive_warp(&c.p_full[buf]);
+    }
+    ok = ok && warp_wait(c, &c.o_full[seg & 1], (seg >> 1) & 1, p.status, kInfoAttnOut);
+    if (softmax_any(group, !ok)) return false;
+    arrive_warp(&c.o_empty[seg & 1]);
+    return true;
+  }
   __device__ void run() {
     Segment s;
     int n = 0, i = 0;
@@ -644,12 +660,8 @@ struct Softmax {
       if (softmax_any(group, !got)) return;
       if (!s.live) return;
       load_queries<kBf16, D>(p, c, q_mem, s, seg);
-      switch ((s.toks * p.G + 15) / 16) {
-        case 1: if (!segment<8>(s, seg, i)) return; break;
-        case 2: if (!segment<16>(s, seg, i)) return; break;
-        case 3: if (!segment<24>(s, seg, i)) return; break;
-        default: if (!segment<32>(s, seg, i)) return;
-      }
+      const int rows = (s.toks * p.G + 15) / 16 * 16, mine = rows <= 8 * kSoftGroups ? 8 : 16;
+      if (group * mine >= rows ? !without_rows(s, seg, i) : mine == 8 ? !segment<8>(s, seg, i) : !segment<16>(s, seg, i)) return;
     }
   }
 };
@@ -685,13 +697,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attention_kv4_kernel(const
     for (int s = 0; s < Geo::kStages; ++s) { mbar_init(&c.kv_full[s], 1); mbar_init(&c.kv_empty[s], 8); }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.k_full[b], 4); mbar_init(&c.k_empty[b], 1);
-      mbar_init(&c.s_full[b], 1); mbar_init(&c.s_empty[b], 8);
+      mbar_init(&c.s_full[b], 1); mbar_init(&c.s_empty[b], 4 * kSoftGroups);
       mbar_init(&c.v_full[b], 4); mbar_init(&c.v_empty[b], 1);
-      mbar_init(&c.p_full[b], 8); mbar_init(&c.p_empty[b], 1);
-      mbar_init(&c.o_full[b], 1); mbar_init(&c.o_empty[b], 8);
+      mbar_init(&c.p_full[b], 4 * kSoftGroups); mbar_init(&c.p_empty[b], 1);
+      mbar_init(&c.o_full[b], 1); mbar_init(&c.o_empty[b], 4 * kSoftGroups);
     }
     for (int s = 0; s < kSegments; ++s) { mbar_init(&c.seg_full[s], 1); mbar_init(&c.seg_empty[s], kReaders); }
-    mbar_init(&c.q_full, 8);
+    mbar_init(&c.q_full, 4 * kSoftGroups);
     mbar_init(&c.drain[0], 1);
     mbar_init(&c.drain[1], 1);
     fence_barrier_init();
@@ -730,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attention_kv4_kernel(const
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     expand<D, false>(p, c, mem + Geo::kRingAt, nullptr, tmem);
-  } else if (warp < 16) {
+  } else if (warp < 8 + 4 * kSoftGroups) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     Softmax<kBf16, D> r{p, c, mem + Geo::kProbsAt, mem + Geo::kQueriesAt, tmem, tid & 127, (warp - 8) / 4, static_cast<uint32_t>((warp & 3) * 32) << 16};
     r.run();

@@ -461,7 +461,9 @@ int resident_clusters(int c) {
   return n;
 }
 
-// CTAs that share a tile: as many as are resident at once, each with 2 blocks at least.
+// CTAs that share a tile: as many as are resident at once, each with 2 blocks at least.  (64
+// x 4096 -> 4096: 21.6 us with one, 15.2 with two, 11.9 with the four that fit; 30 x 4096 ->
+// 1024: 21.0, 14.4 and, with eight, 10.3.)
 int cluster_size(int tiles, int k_blocks, int sms) {
   int c = 1;
   while (c < kMaxCluster && (c + 1) * tiles <= sms && k_blocks / (c + 1) >= 2 && resident_clusters(c + 1) >= tiles) ++c;
