@@ -34,12 +34,19 @@
 // parts in a fixed order: results do not depend on timing.
 //
 // A CTA (one per SM): warp 0 copies tiles (a page of a head is one run of bytes), warps
-// 1 and 2 issue the first and the second products' MMAs, warp 3 walks the list; warps 4..7 expand keys, 8..15 are the softmax, 16..19 expand values.  Every
-// role's code is a short loop: with one warp of a role on a scheduler, what is unrolled
-// runs at the rate at which it is fetched (a tile took 1.7 times as long with the four
-// groups of the expansion unrolled and the rows' width a branch a row instead of a
-// template).  Two warpgroups expanding in turn were no faster (9 tokens of 16 requests: 324
-// us, with one 306).
+// 1 and 2 issue the first and the second products' MMAs, warp 3 walks the list; warps 4..7
+// expand keys, 8..23 are the softmax, 24..27 expand values.  Every role's code is a short
+// loop: with few warps of a role on a scheduler, what is unrolled runs at the rate at which
+// it is fetched (a tile took 1.7 times as long with the four groups of the expansion
+// unrolled).
+//
+// Measured: 8 blocks of 9 tokens over 4096 shared keys and up to 900 own ones 32.3 us; 13
+// blocks of 8 over 30011, D = 64, 81 us; 64 blocks of 9 over 16384 and up to 2000, 347 us,
+// 2250 clocks a tile of 64 rows.  Of those, without the expansion of keys 316, without that
+// of values 307, without the second product 331, without exponentials 343; without any of
+// them 255: what is left is one role waiting for another, at some ten clocks an instruction.
+// A second warpgroup for the values' expansion (338), one for the keys' (360) or issue by
+// whole warps were no faster throughout.
 //
 // Keys past a length are never read as numbers: their codes are replaced by zeros, and
 // their scores before the maximum.
@@ -219,7 +226,7 @@ struct Producer {
   }
 };
 
-// ---------------------------------------------------------------- expansion (warps 4..7 and 16..19)
+// ---------------------------------------------------------------- expansion (warps 4..7 and 24..27)
 // A thread a key: its codes of one kind, as f16.
 template <int D, bool kValues>
 __device__ __forceinline__ void expand(const Kv4Attn& p, Control& c, const uint8_t* ring_mem, uint8_t* v_mem, uint32_t tmem) {
@@ -360,12 +367,12 @@ __device__ __forceinline__ void drain_mma(const Kv4Attn& p, Control& c, int whic
   __syncwarp();
 }
 
-// ---------------------------------------------------------------- softmax (warps 8..11 and 12..15)
-// Two groups of four warps, a half of the rows each, which have nothing to do with one
-// another.  (One group with all rows: a scheduler has one of its warps, whose unrolled code
-// runs as fast as it is fetched; 64 rows took 2500 clocks a tile.)  A group's warps agree on
-// every turn: what one of them alone finds out (a wait that ran out) goes through a vote
-// before any leaves.
+// ---------------------------------------------------------------- softmax (warps 8..23)
+// Four groups of four warps, 8 or 16 of the rows each, which have nothing to do with one
+// another.  A step's waits, votes and loads take longer than the arithmetic of so few rows:
+// two tiles share them.  (64 blocks of 9 tokens: 347 us, with two groups of up to 32 rows,
+// a tile a step, 374; 13 draft blocks 81 and 92.)  A group's warps agree on every turn: what
+// one of them alone finds out (a wait that ran out) goes through a vote before any leaves.
 
 // A segment's queries, by all softmax warps: rows into the K-major, 128-byte-swizzled tile
 // of the first product, in f16, with their scales and limits.  D / 8 lanes take a row; all
@@ -587,8 +594,7 @@ struct Softmax {
   }
 
   // The group's rows of a segment: their number is fixed in the code, as a branch a row
-  // costs more than the row.  Of few rows the waits and the vote of a step take longer than
-  // its arithmetic: two tiles share them.
+  // costs more than the row.
   template <int kMine>
   __device__ __forceinline__ bool segment(const Segment& s, int seg, int& i) {
     const int qb = seg & 1, rows = s.toks * p.G, row0 = group * kMine;

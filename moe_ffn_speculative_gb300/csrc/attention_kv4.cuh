@@ -13,7 +13,10 @@ namespace moe {
 
 constexpr int kTile = 128;       // keys of a unit of work
 constexpr int kRows = 64;        // most rows of a row tile
-constexpr int kItemCost = 4;     // an item's fixed cost, in units (queries, the first reference, its parts)
+// An item's fixed cost in units: queries, the first reference, its parts.  (8 blocks of 9 over
+// 4096 keys and their own: 41.6 us with 0, 35.0 with 2, 32.4 with 4, 35.3 with 8; 16 single
+// tokens over as many: 34.9, 32.8, 28.8 and 28.2.)
+constexpr int kItemCost = 4;
 // What the row's maximum counts when the reference is set, and how far a later score may
 // pass that (powers of two): the largest power is 2^14, a key is held to within 2^-32 of
 // the row's largest.

@@ -583,16 +583,19 @@ cudaError_t launch(const Kv4Attn& p, int rows, cudaStream_t s) {
 
 }  // namespace
 
-// A tile of 128 keys and up to 8 rows costs this kernel about half of what the other
-// needs for up to 64, so it takes a call whose blocks have few rows unless a prefix
-// shared by many of them outweighs their own keys (as far as the tables' sizes tell).
+// A tile of 128 keys costs this kernel 0.55 of what the other needs for up to 64 rows where
+// it has up to 8 (640000 own keys of 16 single tokens: 143 us, the other 257), 0.83 where it
+// has up to 16 (4 tokens each: 212 and 257; at 80000 keys 50 and 48).  So it takes a call
+// whose blocks have few rows unless a prefix shared by many of them outweighs their own keys,
+// as far as the tables' sizes tell (8 blocks of 12 rows over 4096 shared keys and up to 900
+// own ones: 32.8 us here, 27.8 there).
 int kv4_few_rows(int T, int B, int G, int page, int prefix_cap, int table_width) {
   const int block = G * (B > 0 ? ceil_div(T, B) : T);  // rows of a request's block, on average
   if (block > 16) return 0;
   const int rows = block <= 8 ? 8 : 16;
   const long long prefix = tiles_of(prefix_cap * page), own = tiles_of(table_width * page);
   const long long few = ceil_div(T, rows / G), many = ceil_div(T, kRows / G);
-  return prefix * few + B * own <= 2 * (prefix * many + B * own) ? rows : 0;
+  return 5 * (prefix * few + B * own) <= (rows == 8 ? 9 : 6) * (prefix * many + B * own) ? rows : 0;
 }
 
 cudaError_t launch_kv4_few(const Kv4Attn& p, int rows, int D, bool bf16, cudaStream_t s) {
