@@ -526,7 +526,6 @@ __global__ void __launch_bounds__(threads(kBlocks), 1) kv4_few_kernel(const __gr
     for (int s = 0; s < kSegments; ++s) { mbar_init(&c.seg_full[s], 1); mbar_init(&c.seg_empty[s], Geo::kWarps); }
     fence_barrier_init();
   }
-  griddep_launch_dependents();  // kv4_merge_kernel's blocks wait for all of this grid
   griddep_wait();               // what the previous kernel on the stream wrote is visible
   const int plen = find_share<Geo::kThreads>(p, c.start);
   __syncthreads();

@@ -37,7 +37,6 @@ struct BookParams {
   const int32_t* new_len;      // resize
   const int32_t *src, *dst;    // fork
   int n;                       // fork: pairs
-  int signal;                  // the next launch is pages_copy_kernel, which waits for this one's end
   int32_t* status;
   // workspace
   int32_t* count;              // copies
@@ -138,7 +137,6 @@ enum : int { kSkip = -1, kPlain = 0, kSplit = 1 };
 
 __global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid_constant__ BookParams p) {
   __shared__ int n_copies;
-  if (p.signal) griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.B), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
@@ -229,7 +227,6 @@ __global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid
 
 __global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_constant__ BookParams p) {
   __shared__ int n_copies;
-  if (p.signal) griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.n), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
@@ -300,8 +297,8 @@ __global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_c
 }
 
 // The listed pages' bytes in every pool, a chunk a CTA at a time.  128 requests forked (330
-// MB read and written): 69.7 us with the bookkeeping, 4.7 TB/s; with four loads a thread
-// under way instead of eight 73.6, without the streaming hints 70.8.
+// MB read and written): 68.5 us with the bookkeeping, 4.8 TB/s; with four loads a thread
+// under way instead of eight 4 us more, without the streaming hints one.
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
   griddep_wait();
   const int per = p.chunk0[p.n_pools];
@@ -512,7 +509,6 @@ moe_status run_book(void (*kernel)(BookParams), BookParams& b, const moe_page_po
   b.list = reinterpret_cast<int32_t*>(w + L.o_list);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  b.signal = n_pools > 0;
   if (launch(kernel, b, dim3(1), kBookThreads, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (n_pools == 0) return MOE_OK;
   c.n_pools = n_pools;

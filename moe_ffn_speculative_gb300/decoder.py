@@ -174,13 +174,15 @@ class PagedRequests:
         ops.pages_fork(self.refs, self.table, self.own_len, src, dst, self.page, self.ws, self.caches)
 
     def block(self, n: int, prefix_len: Optional[torch.Tensor] = None):
-        """Pages for n more tokens of every request.  -> (Batch of them, the lengths before)."""
+        """Pages for n more tokens of every request.  -> (Batch of them, the lengths before).
+        Tokens of a request that there were no pages for (recorded in `ws`) go to no slot."""
         base = self.own_len.clone()
         self.resize(base + n)
         at = base[:, None] + torch.arange(n, dtype=torch.int32, device=base.device)
         pages = self.table.gather(1, (at // self.page).clamp(max=self.table.shape[1] - 1).long())
         positions = at if prefix_len is None else at + prefix_len
-        return Batch(positions=positions.flatten(), slots=(pages * self.page + at % self.page).flatten(),
+        slots = torch.where(at < self.own_len[:, None], pages * self.page + at % self.page, -1)
+        return Batch(positions=positions.flatten(), slots=slots.flatten(),
                      q_start=torch.arange(len(base) + 1, dtype=torch.int32, device=base.device) * n, own_len=self.own_len,
                      page_table=self.table, prefix_pages=self.prefix_pages, prefix_len=prefix_len), base
 

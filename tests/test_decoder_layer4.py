@@ -167,5 +167,30 @@ def test_steps(captured):
 
 
 @pytest.mark.gpu
+def test_requests_without_pages():
+    """What finds no page is recorded and written nowhere: not into the page that a fork
+    shares, nor past the table."""
+    def i32(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    a = decoder.AttentionConfig(q_heads=4, kv_heads=1, head_dim=64)
+    cache = decoder.KVCache4(3, 8, a)
+    r = decoder.PagedRequests(3, 2, 3, 8, [cache.data])
+    r.resize(i32(5, 8, 0))
+    r.fork(i32(0), i32(2))          # takes the last page
+    assert r.own_len.tolist() == [5, 8, 5] and sorted(r.refs.tolist()) == [1, 1, 1]
+    b, base = r.block(2)            # 5 + 2 fit their pages; 8 + 2 need one that there is not
+    assert base.tolist() == [5, 8, 5] and r.own_len.tolist() == [7, 8, 7]
+    first = r.table[:, 0].tolist()
+    assert b.slots.tolist() == [first[0] * 8 + 5, first[0] * 8 + 6, -1, -1, first[2] * 8 + 5, first[2] * 8 + 6]
+    assert r.ws.device_status()[0] == ops.MOE_ERR_DEVICE_POOL
+    # past the table's end: left alone
+    r = decoder.PagedRequests(1, 2, 3, 8, [cache.data])
+    r.resize(i32(15))
+    b, _ = r.block(2)
+    assert r.own_len.tolist() == [15] and b.slots.tolist() == [-1, -1]
+    assert r.ws.device_status()[0] != ops.MOE_OK
+
+
+@pytest.mark.gpu
 def test_example_runs():
     assert decoder.main4(requests=2, block=3, prefix=100, own=20, steps=3) > 0

@@ -116,3 +116,48 @@ def test_extension_answers_none_to_what_it_does_not_know():
         for n in range(5, 18):
             for x in (None, "x", t, 1.5, (), (t,), [t]):
                 assert f(*[x] * n) is None
+
+
+@pytest.mark.gpu
+def test_two_at_once():
+    """Calls of all kinds on two streams at a time, each with a workspace of its own, give
+    the bits that they give one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(BF)
+    w = ops.q4_prepare(torch.randint(0, 256, (1024, 512), generator=g, device="cuda", dtype=torch.uint8),
+                       normal(1024, 8) * 0.02)
+    cache = _cache(24, 64, 2, 64)
+    starts = {n: torch.arange(5, dtype=torch.int32, device="cuda") * n for n in (1, 9)}
+    prefix, prefix_len = torch.arange(12, dtype=torch.int32, device="cuda"), _i32(700)
+    table, own = torch.arange(12, 24, dtype=torch.int32, device="cuda").view(4, 3), _i32(20, 64, 130, 9)
+    x = {n: normal(4 * n, 1024) for n in (1, 9)}
+
+    def lane():
+        spaces = [ops.Workspace(n) for n in (ops.linear_q4_workspace_bytes(36, 1024, 1024),
+                                             ops.prefix_attention_kv4_workspace_bytes(36, 4, 16, 2, 64), 256)]
+
+        def call(n, stream=None):
+            y = ops.linear_q4(x[n], w, spaces[0], activation="silu", stream=stream)
+            o = ops.prefix_attention_kv4(y.view(4 * n, 16, 64), cache, starts[n], prefix, prefix_len, table, own, spaces[1],
+                                         stream=stream)
+            k, v = ops.kv4_read(cache, 64, spaces[2], pages=prefix, stream=stream)
+            return y, o, k, v
+        return call, spaces
+    lanes, streams = [lane(), lane()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = {n: lanes[0][0](n) for n in (1, 9)}
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                n = (1, 9)[(turn + i) % 2]
+                got.append((n, lanes[i][0](n)))
+    torch.cuda.synchronize()
+    for n, outs in got:
+        for a, b in zip(outs, want[n]):
+            assert torch.equal(a, b)
+    for _, spaces in lanes:
+        for ws in spaces:
+            assert ws.device_status() == (ops.MOE_OK, 0)

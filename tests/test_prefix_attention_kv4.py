@@ -155,6 +155,14 @@ def test_many_blocks(B):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9, 12, 13, 16])
+def test_every_width_over_a_shared_prefix(n):
+    """Row tiles of 4 to 64 rows over own keys of none to four tiles, behind a prefix that
+    keeps them with the kernel for many rows."""
+    Batch4(8, 2, 64, HF, 32, 1500, [(n, max(n, own)) for own in (0, 10, 127, 128, 129, 256, 300, 400)], seed=n).check(True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("page", [64, 16, 512])
 def test_many_tiles_per_row_tile(page):
     """A long context for few rows: split over every SM and joined."""
