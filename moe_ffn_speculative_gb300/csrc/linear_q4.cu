@@ -96,8 +96,8 @@ struct Tiles {
     at = blockIdx.x / p.cluster;
     step = gridDim.x / p.cluster;
     end = p.row_tiles * p.tok_tiles;
-    kb0 = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / p.cluster);
-    kb1 = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / p.cluster);
+    kb0 = rank * p.blocks_each + min(rank, p.blocks_more);
+    kb1 = kb0 + p.blocks_each + (rank < p.blocks_more ? 1 : 0);
   }
 };
 
@@ -158,14 +158,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int groups = kBlock >> p.group_log2;       // of a block
   const Tiles tiles(p, rank);
 
-  if (tid == 0) {
-    c.abort_flag = 0;
-    for (int s = 0; s < p.stages; ++s) { mbar_init(&c.full[s], 1); mbar_init(&c.empty[s], 9); }
-    for (int s = 0; s < kExpanders; ++s) { mbar_init(&c.a_full[s], 4); mbar_init(&c.a_empty[s], 1); }
-    for (int s = 0; s < 2; ++s) { mbar_init(&c.d_full[s], 1); mbar_init(&c.d_empty[s], 8); }
-    mbar_init(&c.drain, 1);
+  if (warp == 0) {
+    if (lane < p.stages) { mbar_init(&c.full[lane], 1); mbar_init(&c.empty[lane], 9); }
+    if (lane < kExpanders) { mbar_init(&c.a_full[lane], 4); mbar_init(&c.a_empty[lane], 1); }
+    if (lane < 2) { mbar_init(&c.d_full[lane], 1); mbar_init(&c.d_empty[lane], 8); }
+    if (lane == 0) {
+      c.abort_flag = 0;
+      mbar_init(&c.drain, 1);
+      tma_prefetch_desc(&tm_x);
+    }
     fence_barrier_init();
-    tma_prefetch_desc(&tm_x);
   }
   if (warp == 1) {
     tmem_alloc(&c.tmem, 512);
@@ -324,12 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.cluster > 1) {
         // token-major over the stages (every copy and product is complete: a cluster has one tile)
         float* part = reinterpret_cast<float*>(mem) + row;
-        for (int i = first; i < toks; i += 32) {
-          uint32_t v[16];
-          tmem_ld16(src + i, v);
+        for (int i = first; i < toks; i += 64) {
+          uint32_t v[2][16];
+          tmem_ld16(src + i, v[0]);
+          if (i + 32 < toks) tmem_ld16(src + i + 32, v[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) part[(i + k) * kRows] = __uint_as_float(v[k]);
+          for (int k = 0; k < 16; ++k) part[(i + k) * kRows] = __uint_as_float(v[0][k]);
+          if (i + 32 < toks)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) part[(i + 32 + k) * kRows] = __uint_as_float(v[1][k]);
         }
       } else {
         const int n = t % p.row_tiles * kRows + row;
@@ -380,10 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = ta + i * kWarps;
       if (t < tb && n < p.N) finish4<kBf16>(p, v[i], b, res[i], p.y + (t0 + t) * p.y_stride + n);
     }
+    __threadfence();
     cluster_wait();  // the others have read this CTA's sums
   }
   // (y may be what a fused forward loads before it waits: see linear.cu)
-  __threadfence();
+  if (p.cluster == 1) __threadfence();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -585,6 +592,8 @@ moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const 
   const long long tiles = static_cast<long long>(p.row_tiles) * p.tok_tiles;
   if (tiles > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   p.cluster = cluster_size(static_cast<int>(tiles < sms ? tiles : sms), p.k_blocks, sms);
+  p.blocks_each = p.k_blocks / p.cluster;
+  p.blocks_more = p.k_blocks % p.cluster;
   p.stages = (kSmem - 1024) / (p.n_tok * kBlock * 2 + ceil_div(p.block_bytes, 1024) * 1024);
   if (p.stages > kQ4Stages) p.stages = kQ4Stages;
   CUtensorMap tm_x;
