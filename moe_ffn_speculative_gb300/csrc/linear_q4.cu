@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
   const uint32_t x_bytes = p.n_tok * kBlock * 2, w_space = (p.block_bytes + 1023) / 1024 * 1024;
   const uint32_t stage_space = x_bytes + w_space;  // the token tile first: it is swizzled
+  float* sums = reinterpret_cast<float*>(mem + p.stages * stage_space);  // of a cluster: [rank][slots][kRows]
   const int groups = kBlock >> p.group_log2;       // of a block
   const Tiles tiles(p, rank);
 
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.cluster > 1) cluster_arrive();  // (this CTA runs: the others may write to its memory)
   const uint32_t tmem = c.tmem;
   // the first blocks come into L2 while the previous kernel ends (what it writes, weights
   // included, is read only after it)
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring r;
       uint32_t a_phase = 0, turn = 0, tile = 0;
       for (int t = tiles.at; t < tiles.end && ok; t += tiles.step, ++tile) {
-        const uint32_t sums = tmem + kSumsCol + (tile & 1) * kMaxTok;
+        const uint32_t d = tmem + kSumsCol + (tile & 1) * kMaxTok;
         ok = warp_wait(c, &c.d_empty[tile & 1], (tile >> 1 & 1) ^ 1u, p.status, kInfoAccEmpty);
         if (!ok) break;
         uint32_t more = 0;
@@ -243,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool next = mbar_test_wait(&c.a_full[a_next], next_phase);
 #pragma unroll
             for (int i = 0; i < kHalf / 16; ++i) {
-              mma_ts_by(lead, sums, a + i * 8, b + i * 2, id, i ? 1u : more);
-              mma_ts_by(lead, sums, a + kHalf / 2 + i * 8, b + i * 2, id | kNegateA, 1u);
+              mma_ts_by(lead, d, a + i * 8, b + i * 2, id, i ? 1u : more);
+              mma_ts_by(lead, d, a + kHalf / 2 + i * 8, b + i * 2, id | kNegateA, 1u);
             }
             more = 1u;
             mma_commit_by(lead, &c.a_empty[turn]);
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127, first = (warp / 4 - 1 - kExpanders) * 16;
     const uint32_t lanes = tmem + kSumsCol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint32_t tile = 0;
+    if (p.cluster > 1) cluster_wait();
     for (int t = tiles.at; t < tiles.end && ok; t += tiles.step, ++tile) {
       ok = warp_wait(c, &c.d_full[tile & 1], tile >> 1 & 1, p.status, kInfoAccFull);
       if (!ok) break;
@@ -324,18 +327,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = t / p.row_tiles * p.n_tok, toks = min(p.n_tok, p.M - t0);
       const uint32_t src = lanes + (tile & 1) * kMaxTok;
       if (p.cluster > 1) {
-        // token-major over the stages (every copy and product is complete: a cluster has one tile)
-        float* part = reinterpret_cast<float*>(mem) + row;
-        for (int i = first; i < toks; i += 64) {
-          uint32_t v[2][16];
-          tmem_ld16(src + i, v[0]);
-          if (i + 32 < toks) tmem_ld16(src + i + 32, v[1]);
+        // the c-th 8 tokens' sums to rank c % cluster, which adds up what the ranks write there
+        int q = first / 8, slot = 0;
+        for (int i = first; i < toks; i += 32, q += 2) {
+          uint32_t v[16];
+          tmem_ld16(src + i, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) part[(i + k) * kRows] = __uint_as_float(v[0][k]);
-          if (i + 32 < toks)
+          for (int h = 0; h < 2; ++h, ++q) {
+            while (q >= p.cluster) { q -= p.cluster; slot += 8; }
+            const uint32_t to = of_rank(smem_u32(sums + (rank * p.slots + slot) * kRows + row), q);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) part[(i + 32 + k) * kRows] = __uint_as_float(v[1][k]);
+            for (int k = 0; k < 8; ++k) st_cluster(to + k * kRows * 4, __uint_as_float(v[8 * h + k]));
+          }
         }
       } else {
         const int n = t % p.row_tiles * kRows + row;
@@ -354,43 +358,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (p.cluster > 1) {
-    // this CTA's share of the tokens, a warp a token and a lane 4 outputs; what the epilogue
-    // reads comes while the others finish
+    if (warp < 4 + 4 * kExpanders) cluster_wait();
+    // this CTA's tokens, a warp each and a lane 4 outputs; what the epilogue reads comes while
+    // the others finish
     constexpr int kWarps = kThreads / 32, kEach = (kMaxTok / 2 + kWarps - 1) / kWarps;
     const int n = tiles.at % p.row_tiles * kRows + lane * 4, t0 = tiles.at / p.row_tiles * p.n_tok;
     const int toks = min(p.n_tok, p.M - t0);
-    const int ta = toks * rank / p.cluster + warp, tb = toks * (rank + 1) / p.cluster;
     ushort4 b = make_ushort4(0, 0, 0, 0), res[kEach];
     if (p.bias && n < p.N) b = __ldg(reinterpret_cast<const ushort4*>(p.bias + n));
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int t = ta + i * kWarps;
+      const int slot = warp + i * kWarps, t = ((slot >> 3) * p.cluster + rank) * 8 + (slot & 7);
       res[i] = make_ushort4(0, 0, 0, 0);
-      if (p.residual && n < p.N && t < tb) res[i] = *reinterpret_cast<const ushort4*>(p.residual + (t0 + t) * p.res_stride + n);
+      if (p.residual && n < p.N && slot < p.slots && t < toks) res[i] = *reinterpret_cast<const ushort4*>(p.residual + (t0 + t) * p.res_stride + n);
     }
     cluster_sync();
-    const uint32_t part = smem_u32(mem) + (ta * kRows + lane * 4) * 4;
-    float4 v[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q = 0; q < p.cluster; ++q)
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (ta + i * kWarps < tb) {
-          const float4 f = ld_cluster4(part + i * kWarps * kRows * 4, q);
-          v[i].x += f.x; v[i].y += f.y; v[i].z += f.z; v[i].w += f.w;
-        }
-    cluster_arrive();
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int t = ta + i * kWarps;
-      if (t < tb && n < p.N) finish4<kBf16>(p, v[i], b, res[i], p.y + (t0 + t) * p.y_stride + n);
+      const int slot = warp + i * kWarps, t = ((slot >> 3) * p.cluster + rank) * 8 + (slot & 7);
+      if (slot >= p.slots || t >= toks || n >= p.N) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < p.cluster; ++q) {
+        const float4 f = *reinterpret_cast<const float4*>(sums + (q * p.slots + slot) * kRows + lane * 4);
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+      }
+      finish4<kBf16>(p, v, b, res[i], p.y + (t0 + t) * p.y_stride + n);
     }
-    __threadfence();
-    cluster_wait();  // the others have read this CTA's sums
   }
   // (y may be what a fused forward loads before it waits: see linear.cu)
-  if (p.cluster == 1) __threadfence();
+  __threadfence();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -594,7 +590,8 @@ moe_status moe_linear_q4(const void* x, long long x_stride, int M, int K, const 
   p.cluster = cluster_size(static_cast<int>(tiles < sms ? tiles : sms), p.k_blocks, sms);
   p.blocks_each = p.k_blocks / p.cluster;
   p.blocks_more = p.k_blocks % p.cluster;
-  p.stages = (kSmem - 1024) / (p.n_tok * kBlock * 2 + ceil_div(p.block_bytes, 1024) * 1024);
+  p.slots = p.cluster > 1 ? ceil_div(p.n_tok / 8, p.cluster) * 8 : 0;
+  p.stages = (kSmem - 1024 - p.slots * p.cluster * kRows * 4) / (p.n_tok * kBlock * 2 + ceil_div(p.block_bytes, 1024) * 1024);
   if (p.stages > kQ4Stages) p.stages = kQ4Stages;
   CUtensorMap tm_x;
   const uint64_t xd[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(M)};

@@ -25,6 +25,7 @@ struct Q4Params {
   int block_bytes;           // of a weight block
   int n_tok, row_tiles, tok_tiles;
   int stages, cluster;
+  int slots;                     // tokens of a tile that a CTA of the cluster finishes, at most
   int blocks_each, blocks_more;  // of a tile's K a CTA of the cluster takes; those that take one more
   const uint8_t* w;
   const uint16_t *bias, *residual;
