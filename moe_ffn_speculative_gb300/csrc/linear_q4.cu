@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.cluster > 1) cluster_arrive();  // (this CTA runs: the others may write to its memory)
+  if (p.cluster > 1) cluster_arrive_relaxed();  // the others may write to its memory
   const uint32_t tmem = c.tmem;
   // the first blocks come into L2 while the previous kernel ends (what it writes, weights
   // included, is read only after it)
