@@ -319,38 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127, first = (warp / 4 - 1 - kExpanders) * 16;
     const uint32_t lanes = tmem + kSumsCol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint32_t tile = 0;
-    if (p.cluster > 1) cluster_wait();
-    for (int t = tiles.at; t < tiles.end && ok; t += tiles.step, ++tile) {
+    for (int t = tiles.at; t < tiles.end && ok && p.cluster == 1; t += tiles.step, ++tile) {
       ok = warp_wait(c, &c.d_full[tile & 1], tile >> 1 & 1, p.status, kInfoAccFull);
       if (!ok) break;
       tc_fence_after();
       const int t0 = t / p.row_tiles * p.n_tok, toks = min(p.n_tok, p.M - t0);
       const uint32_t src = lanes + (tile & 1) * kMaxTok;
-      if (p.cluster > 1) {
-        // the c-th 8 tokens' sums to rank c % cluster, which adds up what the ranks write there
-        int q = first / 8, slot = 0;
-        for (int i = first; i < toks; i += 32, q += 2) {
-          uint32_t v[16];
-          tmem_ld16(src + i, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < 2; ++h, ++q) {
-            while (q >= p.cluster) { q -= p.cluster; slot += 8; }
-            const uint32_t to = of_rank(smem_u32(sums + (rank * p.slots + slot) * kRows + row), q);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) st_cluster(to + k * kRows * 4, __uint_as_float(v[8 * h + k]));
-          }
-        }
-      } else {
-        const int n = t % p.row_tiles * kRows + row;
-        const float b = p.bias && n < p.N ? to_f<kBf16>(p.bias[n]) : 0.f;
-        for (int i = first; i < toks; i += 32) {
-          uint32_t v[16];
-          tmem_ld16(src + i, v);
-          tmem_ld_wait();
-          if (n < p.N) finish16<kBf16>(p, v, b, t0 + i, min(16, toks - i), n);
-          __syncwarp();
-        }
+      const int n = t % p.row_tiles * kRows + row;
+      const float b = p.bias && n < p.N ? to_f<kBf16>(p.bias[n]) : 0.f;
+      for (int i = first; i < toks; i += 32) {
+        uint32_t v[16];
+        tmem_ld16(src + i, v);
+        tmem_ld_wait();
+        if (n < p.N) finish16<kBf16>(p, v, b, t0 + i, min(16, toks - i), n);
+        __syncwarp();
       }
       tc_fence_before();
       arrive_warp(&c.d_empty[tile & 1]);
@@ -358,12 +340,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (p.cluster > 1) {
-    if (warp < 4 + 4 * kExpanders) cluster_wait();
+    // the c-th 8 tokens' sums to rank c % cluster, which adds up what the ranks write there: all
+    // warpgroups but the first, 16 tokens at a time
+    const int toks = min(p.n_tok, p.M - tiles.at / p.row_tiles * p.n_tok);
+    cluster_wait();
+    if (warp >= 4 && ok && warp_wait(c, &c.d_full[0], 0, p.status, kInfoAccFull)) {
+      tc_fence_after();
+      const uint32_t src = tmem + kSumsCol + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      int q = (warp / 4 - 1) * 2, slot = 0;
+      for (int i = q * 8; i < toks; i += (kThreads / 128 - 1) * 16, q += (kThreads / 128 - 2) * 2) {
+        uint32_t v[16];
+        tmem_ld16(src + i, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 2; ++h, ++q) {
+          while (q >= p.cluster) { q -= p.cluster; slot += 8; }
+          const uint32_t to = of_rank(smem_u32(sums + (rank * p.slots + slot) * kRows + (tid & 127)), q);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) st_cluster(to + k * kRows * 4, __uint_as_float(v[8 * h + k]));
+        }
+      }
+      tc_fence_before();
+    }
     // this CTA's tokens, a warp each and a lane 4 outputs; what the epilogue reads comes while
     // the others finish
     constexpr int kWarps = kThreads / 32, kEach = (kMaxTok / 2 + kWarps - 1) / kWarps;
     const int n = tiles.at % p.row_tiles * kRows + lane * 4, t0 = tiles.at / p.row_tiles * p.n_tok;
-    const int toks = min(p.n_tok, p.M - t0);
     ushort4 b = make_ushort4(0, 0, 0, 0), res[kEach];
     if (p.bias && n < p.N) b = __ldg(reinterpret_cast<const ushort4*>(p.bias + n));
 #pragma unroll
