@@ -121,6 +121,16 @@ __global__ void __launch_bounds__(kFewThreads, kTiles == 1 ? 2 : 1)
             for (int i = 0; i < 4; ++i) acc[h][j][i] = fmaf(sum[h][j][i], s[2 * h + (i >> 1)], acc[h][j][i]);
     }
   }
+  // (what the epilogue reads is on its way while the warps meet)
+  constexpr int kEach = (kTiles * 8 + kWarps - 1) / kWarps;
+  const int n = n0 + lane;
+  uint16_t bias = 0, res[kEach] = {};
+  if (n < p.N) {
+    if (p.bias) bias = p.bias[n];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (p.residual && warp + i * kWarps < p.M) res[i] = p.residual[(warp + i * kWarps) * p.res_stride + n];
+  }
   // token 8 j + 2 t + (i & 1), row 16 h + g + 8 (i >> 1)
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -130,15 +140,17 @@ __global__ void __launch_bounds__(kFewThreads, kTiles == 1 ? 2 : 1)
       for (int i = 0; i < 4; ++i)
         sums[((warp * kTiles + j) * 8 + 2 * t + (i & 1)) * kPad + 16 * h + g + 8 * (i >> 1)] = acc[h][j][i];
   __syncthreads();
-  const int n = n0 + lane;
   if (n < p.N)
-    for (int m = warp; m < p.M; m += kWarps) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int m = warp + e * kWarps;
+      if (m >= p.M) break;
       float v = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) v += sums[(i * kTiles * 8 + m) * kPad + lane];
-      if (p.bias) v += to_f<kBf16>(p.bias[n]);
+      if (p.bias) v += to_f<kBf16>(bias);
       v = activate(v, p.act);
-      if (p.residual) v += to_f<kBf16>(p.residual[m * p.res_stride + n]);
+      if (p.residual) v += to_f<kBf16>(res[e]);
       p.y[m * p.y_stride + n] = from_f<kBf16>(v);
     }
   __threadfence();  // (y may be what a fused forward loads before it waits: see linear.cu)
