@@ -17,16 +17,17 @@
 // A CTA (one per SM): warp 0 copies weight blocks and token tiles into a ring of stages,
 // warp 1 issues the MMAs, warpgroups 1 to 4 expand half a block each in turn, and
 // warpgroups 5 and 6 run a tile's epilogue under the next one's products (one group: gelu took
-// 317 us there).  Few tiles are shared by clusters of CTAs, each a range of K, whose sums meet
-// in distributed shared memory in rank order; of many, each CTA takes its share one after the
+// 317 us there).  Few tiles are shared by clusters of CTAs, each a range of K: the sums are
+// written to the shared memory of the CTA that adds them up in rank order; of many, each CTA takes its share one after the
 // other.
 //
 // Measured (floors in brackets): 2048 x 4096 x 12288, groups of 64, gelu, 236 us (106; the
 // tensor cores' doubled work is 1.74 PFLOP/s, 0.9 of the measured cuBLAS rate); 72 x 4096 ->
-// 6144 15.9 us (2.2), 64 x 4096 -> 4096 11.9.  There 6 us are prologue, fill and the cluster's
+// 6144 14.9 us (2.2), 64 x 4096 -> 4096 10.6.  There 5 us are prologue, fill and the cluster's
 // meeting, the rest 0.55 us a block: of it without stores to tensor memory 0.4, without
 // the arithmetic 0.42, without MMAs 0.5, with none of them 0.32, which is waits and issue.
-// Six buffers of expanded weights in place of four made no difference.
+// Six buffers of expanded weights in place of four, or two warps that issue, each with sums of
+// its own, were not faster.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -467,8 +468,8 @@ int resident_clusters(int c) {
 }
 
 // CTAs that share a tile: as many as are resident at once, each with 2 blocks at least.  (64
-// x 4096 -> 4096: 21.6 us with one, 15.2 with two, 11.9 with the four that fit; 30 x 4096 ->
-// 1024: 21.0, 14.4 and, with eight, 10.3.)
+// x 4096 -> 4096: 21.6 us with one, 15.2 with two, 10.6 with the four that fit; 30 x 4096 ->
+// 1024: 21.0, 14.4 and, with eight, 7.7.)
 int cluster_size(int tiles, int k_blocks, int sms) {
   int c = 1;
   while (c < kMaxCluster && (c + 1) * tiles <= sms && k_blocks / (c + 1) >= 2 && resident_clusters(c + 1) >= tiles) ++c;

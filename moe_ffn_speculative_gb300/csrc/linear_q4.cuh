@@ -36,8 +36,8 @@ struct Q4Params {
 };
 
 // For few rows (linear_q4_few.cu): a kernel on the warps' own matrix instructions.  Where the
-// two cross (us, this kernel and the other): 1 row of 4096 x 4096 6.2 and 11.9, 24 rows 7.2
-// and 11.8, 32 rows 9.7 and 11.8; of 4096 x 24576 20.7 and 42.5, 37.0 and 43.8, 48.2 and 43.9.
+// two cross (us, this kernel and the other): 1 row of 4096 x 4096 5.4 and 9.8, 24 rows 7.7
+// and 9.8; of 4096 x 24576 17.5 and 37, 31.5 and 37; 32 rows 9.7 and 10, 48 and 37.
 constexpr int kQ4FewRows = 24;
 cudaError_t launch_linear_q4_few(bool f16, const Q4Params& p, const void* x, long long x_stride, cudaStream_t s);
 

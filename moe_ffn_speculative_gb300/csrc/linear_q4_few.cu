@@ -8,12 +8,13 @@
 // same places are their other side: neither passes shared memory.  A group's fp32 sums
 // are whole numbers times inputs; its scales multiply them as they are added up.
 //
-// A CTA takes 32 weight rows, its 16 warps a block of 128 inputs each in turn, 16 rows a
+// A CTA takes 32 weight rows, its 16 or 8 warps a block of 128 inputs each in turn, 16 rows a
 // fragment; the warps' sums meet in shared memory in the warps' order.  (Fewer rows a warp
 // would read the tokens' inputs more often, more would leave SMs without work at 4096 rows.)
 //
-// Measured: 1 row of 4096 x 4096 6.2 us (floor 1.3: launch, two dependent trips to memory and
-// the joining), 4096 x 24576 20.7 us (2.6 TB/s), 16 rows 30.8.
+// Measured: 1 row of 4096 x 4096 5.4 us (floor 1.3: launch, two dependent trips to memory and
+// the joining), 4096 x 24576 17.5 us (3.0 TB/s), 16 rows 24.7: the pipe that expands is busy a
+// third of the time, memory less; a warp's loads do not run under its own arithmetic.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -25,7 +26,6 @@
 namespace moe {
 namespace {
 
-constexpr int kFewThreads = 512, kWarps = kFewThreads / 32;
 constexpr int kWarpRows = 32;
 constexpr int kPad = kWarpRows + 4;  // floats a token of a warp's sums (no bank twice)
 
@@ -52,8 +52,8 @@ __device__ __forceinline__ uint32_t load_once(const void* p) {
 }
 
 // kTiles: 8 tokens each.
-template <bool kBf16, int kTiles>
-__global__ void __launch_bounds__(kFewThreads, kTiles == 1 ? 2 : 1)
+template <bool kBf16, int kTiles, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (kTiles == 1 ? 32 : 16) / kWarps)
     linear_q4_few_kernel(const __grid_constant__ Q4Params p, const uint16_t* x, long long x_stride) {
   extern __shared__ float sums[];  // [warps][tokens][kPad]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -156,35 +156,45 @@ __global__ void __launch_bounds__(kFewThreads, kTiles == 1 ? 2 : 1)
   __threadfence();  // (y may be what a fused forward loads before it waits: see linear.cu)
 }
 
-template <bool kBf16, int kTiles>
+template <bool kBf16, int kTiles, int kWarps>
 cudaError_t launch_few(const Q4Params& p, const uint16_t* x, long long x_stride, cudaStream_t s) {
   constexpr int kBytes = kWarps * kTiles * 8 * kPad * 4;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(linear_q4_few_kernel<kBf16, kTiles>, kBytes, done);
+  const cudaError_t e = allow_smem(linear_q4_few_kernel<kBf16, kTiles, kWarps>, kBytes, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.dynamicSmemBytes = kBytes;
   cfg.gridDim = dim3(ceil_div(p.N, kWarpRows));
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_q4_few_kernel<kBf16, kTiles>, p, x, x_stride);
+  return cudaLaunchKernelEx(&cfg, linear_q4_few_kernel<kBf16, kTiles, kWarps>, p, x, x_stride);
+}
+
+// With 16 warps a CTA the weights of one are read soonest, with 8 more of them are at work at
+// once.  (1 row of 4096 x 4096: 5.4 and 6.2 us, x 12288: 11.3 and 10.3, x 24576: 19.3 and 17.5;
+// 16 rows: x 6144 10.8 and 9.3, x 24576 30.3 and 24.7; 12288 x 4096: 10.8 and 12.9.)
+template <int kWarps>
+cudaError_t launch_few(bool f16, const Q4Params& p, const uint16_t* x, long long x_stride, cudaStream_t s) {
+  switch (ceil_div(p.M, 8)) {
+    case 1: return f16 ? launch_few<false, 1, kWarps>(p, x, x_stride, s) : launch_few<true, 1, kWarps>(p, x, x_stride, s);
+    case 2: return f16 ? launch_few<false, 2, kWarps>(p, x, x_stride, s) : launch_few<true, 2, kWarps>(p, x, x_stride, s);
+    default: return f16 ? launch_few<false, 3, kWarps>(p, x, x_stride, s) : launch_few<true, 3, kWarps>(p, x, x_stride, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_q4_few(bool f16, const Q4Params& p, const void* x, long long x_stride, cudaStream_t s) {
   const uint16_t* xs = static_cast<const uint16_t*>(x);
-  switch (ceil_div(p.M, 8)) {
-    case 1: return f16 ? launch_few<false, 1>(p, xs, x_stride, s) : launch_few<true, 1>(p, xs, x_stride, s);
-    case 2: return f16 ? launch_few<false, 2>(p, xs, x_stride, s) : launch_few<true, 2>(p, xs, x_stride, s);
-    default: return f16 ? launch_few<false, 3>(p, xs, x_stride, s) : launch_few<true, 3>(p, xs, x_stride, s);
-  }
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorUnknown;
+  return ceil_div(p.N, kWarpRows) > sms ? launch_few<8>(f16, p, xs, x_stride, s) : launch_few<16>(f16, p, xs, x_stride, s);
 }
 
 }  // namespace moe
