@@ -352,27 +352,30 @@ struct Warp {
       }
   }
 
-  // O^T of 16 keys.  Two keys' pairs of channels are exchanged into channels' pairs of keys.
+  // O^T of 16 keys.  Two keys' codes are exchanged, so that a byte holds a channel of both.
   __device__ __forceinline__ void outputs(const RawValues<D>& x, const uint32_t (&pb)[kBlocks][2]) {
-    uint32_t f[4];
+    uint32_t f[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = scale2(x.s[i]);
+    for (int i = 0; i < 2; ++i)
+      f[i] = pack_h2(__uint_as_float(x.s[2 * i] << 23), __uint_as_float(x.s[2 * i + 1] << 23));
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
-      uint32_t h[4][4];
+      uint32_t a[4][4];  // even and odd channels of keys q and 4 + q, then of 8 + q and 12 + q
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kv4_expand(x.v[i][w], h[i]);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t u = x.v[2 * i][w], v = x.v[2 * i + 1][w];
+        kv4_expand((u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u), a[2 * i]);
+        kv4_expand(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), a[2 * i + 1]);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) h[i][b] = kv4_mul2(h[i][b], f[i]);
+        for (int b = 0; b < 4; ++b) {
+          a[2 * i][b] = kv4_mul2(a[2 * i][b], f[i]);
+          a[2 * i + 1][b] = kv4_mul2(a[2 * i + 1][b], f[i]);
+        }
       }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint32_t a0 = __byte_perm(h[0][b], h[1][b], 0x5410), a1 = __byte_perm(h[0][b], h[1][b], 0x7632);
-        const uint32_t a2 = __byte_perm(h[2][b], h[3][b], 0x5410), a3 = __byte_perm(h[2][b], h[3][b], 0x7632);
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int n = 0; n < kBlocks; ++n) mma(o[n][4 * w + b], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-      }
+        for (int n = 0; n < kBlocks; ++n) mma(o[n][4 * w + b], a[0][b], a[1][b], a[2][b], a[3][b], pb[n][0], pb[n][1]);
     }
   }
 
