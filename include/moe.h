@@ -23,7 +23,8 @@
  *
  * Around the layer, at the end of this file: the attention side of the same
  * decoder layer (q/k norms with rotation and cache write, attention over a
- * shared prefix and own pages, projections with their epilogue).
+ * shared prefix and own pages, projections with their epilogue), its forms in 4
+ * bits (projections, cache, attention over it), and the pages of a cache.
  *
  * Conventions (every entry point):
  *   - Every tensor pointer is a DEVICE pointer owned by the caller; tensors are

@@ -586,8 +586,8 @@ cudaError_t launch(const Kv4Attn& p, int rows, cudaStream_t s) {
 }  // namespace
 
 // A tile of 128 keys costs this kernel 0.55 of what the other needs for up to 64 rows where
-// it has up to 8 (640000 own keys of 16 single tokens: 143 us, the other 257), 0.83 where it
-// has up to 16 (4 tokens each: 212 and 257; at 80000 keys 50 and 48).  So it takes a call
+// it has up to 8 (640000 own keys of 16 single tokens: 139 us, the other 257), 0.81 where it
+// has up to 16 (4 tokens each: 209 and 257; at 80000 keys 50 and 48).  So it takes a call
 // whose blocks have few rows unless a prefix shared by many of them outweighs their own keys,
 // as far as the tables' sizes tell (8 blocks of 12 rows over 4096 shared keys and up to 900
 // own ones: 32.8 us here, 27.8 there).
