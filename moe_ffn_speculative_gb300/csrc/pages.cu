@@ -11,12 +11,13 @@
 // A call's bookkeeping is one CTA: a prefix sum over the requests' needs, then a
 // walk over refs from page 0 until as many free pages are found as are needed.  It
 // is bound by latency (a few dependent reads of the tables).  The pages to copy
-// (each is rare in a resize, one a child in a fork) go to a list that a second
-// launch works off over all SMs, bound by the bytes: its grid is fixed, as the
-// list's length is known on the device only.
+// (each is rare in a resize, one a child in a fork) go to a list that the rest of the
+// CTA's cluster works off, or a second launch over all SMs, bound by the bytes: its grid is
+// fixed, as the list's length is known on the device only.
 #include <limits.h>
 #include <string.h>
 
+#include "epilogue.cuh"
 #include "kv4.cuh"
 #include "moe.h"
 
@@ -27,6 +28,8 @@ constexpr int kBookThreads = 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = kCopyThreads * 8 * 16;  // bytes a CTA copies at a time
 constexpr int kCompactThreads = 128;
+constexpr int kCopyCluster = 8;
+constexpr long long kFewBytes = 4ll << 20;
 
 struct BookParams {
   int32_t* refs;
@@ -135,9 +138,8 @@ __device__ __forceinline__ int threads_each(int items) {
 
 enum : int { kSkip = -1, kPlain = 0, kSplit = 1 };
 
-__global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid_constant__ BookParams p) {
+__device__ void resize_book(const BookParams& p) {
   __shared__ int n_copies;
-  griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.B), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
   if (tid == 0) n_copies = 0;
@@ -225,9 +227,8 @@ __global__ void __launch_bounds__(kBookThreads) pages_resize_kernel(const __grid
   if (tid == 0) *p.count = n_copies;
 }
 
-__global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_constant__ BookParams p) {
+__device__ void fork_book(const BookParams& p) {
   __shared__ int n_copies;
-  griddep_wait();
   const int tid = threadIdx.x, each = threads_each(p.n), sub = tid % each, groups = kBookThreads / each;
   const int cap = p.width << p.page_log2;
   if (tid == 0) n_copies = 0;
@@ -296,15 +297,13 @@ __global__ void __launch_bounds__(kBookThreads) pages_fork_kernel(const __grid_c
   if (tid == 0) *p.count = n_copies;
 }
 
-// The listed pages' bytes in every pool, a chunk a CTA at a time.  128 requests forked (330
-// MB read and written): 68.5 us with the bookkeeping, 4.8 TB/s; with four loads a thread
-// under way instead of eight 4 us more, without the streaming hints one.
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
-  griddep_wait();
+// The listed pages' bytes in every pool: chunks first, first + step, .. by kCopyThreads
+// threads, of which this is the tid-th.
+__device__ __forceinline__ void copy_pages(const CopyParams& p, int first, int step, int tid) {
   const int per = p.chunk0[p.n_pools];
-  const long long units = static_cast<long long>(*p.count) * per;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int2 c = p.copies[u / per];
+  const long long units = static_cast<long long>(__ldcg(p.count)) * per;
+  for (long long u = first; u < units; u += step) {
+    const int2 c = __ldcg(p.copies + u / per);
     const int chunk = static_cast<int>(u % per);
     int k = 0;
     while (chunk >= p.chunk0[k + 1]) ++k;
@@ -315,14 +314,42 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
     uint4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int o = (i * kCopyThreads + threadIdx.x) * 16;
+      const int o = (i * kCopyThreads + tid) * 16;
       if (o < left) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + o));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int o = (i * kCopyThreads + threadIdx.x) * 16;
+      const int o = (i * kCopyThreads + tid) * 16;
       if (o < left) __stcs(reinterpret_cast<uint4*>(dst + o), v[i]);
     }
+  }
+}
+// Over all SMs.  128 requests forked (330 MB read and written): 68.5 us with the bookkeeping,
+// 4.8 TB/s; with four loads a thread under way instead of eight 4 us more, without the
+// streaming hints one.
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
+  griddep_wait();
+  copy_pages(p, blockIdx.x, gridDim.x, threadIdx.x);
+}
+
+// The bookkeeping alone (a CTA), or with its copies (a cluster, which does them once its
+// first CTA has listed them: one launch in place of two, but the copies on 8 SMs).  A
+// resize copies only what goes on being written while another request shares it, mostly
+// nothing: 8 requests in 5 pools take 3.9 us like this and 5.4 with two launches; if all of
+// them copy a page (2.8 MB), 13.3 and 7.1.  So it is taken where no more than kFewBytes can
+// have to be copied; a fork, which always copies, has two launches.
+template <bool kFork, bool kCopies>
+__global__ void __launch_bounds__(kBookThreads) pages_book_kernel(const __grid_constant__ BookParams b, const __grid_constant__ CopyParams c) {
+  griddep_wait();
+  if (!kCopies || cluster_rank() == 0) {
+    if (kFork) fork_book(b);
+    else resize_book(b);
+  }
+  if (kCopies) {
+    constexpr int kTeams = kBookThreads / kCopyThreads;
+    cluster_sync();
+    copy_pages(c, static_cast<int>(cluster_rank()) * kTeams + threadIdx.x / kCopyThreads, kCopyCluster * kTeams,
+               threadIdx.x % kCopyThreads);
   }
 }
 
@@ -472,23 +499,28 @@ moe_status check_pools(const moe_page_pool* pools, int n_pools, int n_pages, int
   return MOE_OK;
 }
 
-template <typename P>
-cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, int threads, cudaStream_t s) {
+template <typename... P>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int cluster, cudaStream_t s, const P&... p) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p...);
 }
 
 // One kind of bookkeeping and the copies that it lists.
-moe_status run_book(void (*kernel)(BookParams), BookParams& b, const moe_page_pool* pools, int n_pools,
+template <bool kFork>
+moe_status run_book(BookParams& b, const moe_page_pool* pools, int n_pools,
                     const RowSet* sets, int n_sets, void* ws, size_t ws_bytes, cudaStream_t stream) {
   for (int i = 0; i < n_sets; ++i)
     for (int j = 0; j < i; ++j)
@@ -509,16 +541,22 @@ moe_status run_book(void (*kernel)(BookParams), BookParams& b, const moe_page_po
   b.list = reinterpret_cast<int32_t*>(w + L.o_list);
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  if (launch(kernel, b, dim3(1), kBookThreads, stream) != cudaSuccess) return MOE_ERR_CUDA;
-  if (n_pools == 0) return MOE_OK;
   c.n_pools = n_pools;
+  long long most = 0;  // bytes that a resize may have to copy
   for (int i = 0; i < n_pools; ++i) {
     const long long chunks = (c.pool[i].page_bytes + kCopyChunk - 1) / kCopyChunk;
     c.chunk0[i + 1] = c.chunk0[i] + static_cast<int>(chunks);
+    most += c.pool[i].page_bytes * b.B;
   }
   c.count = b.count;
   c.copies = b.copies;
-  return launch(pages_copy_kernel, c, dim3(8 * sms), kCopyThreads, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (!kFork && n_pools > 0 && most <= kFewBytes)
+    return launch(pages_book_kernel<false, true>, dim3(kCopyCluster), kBookThreads, kCopyCluster, stream, b, c) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  if (launch(pages_book_kernel<kFork, false>, dim3(1), kBookThreads, 1, stream, b, c) != cudaSuccess) return MOE_ERR_CUDA;
+  if (n_pools == 0) return MOE_OK;
+  return launch(pages_copy_kernel, dim3(8 * sms), kCopyThreads, 1, stream, c) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -546,7 +584,7 @@ moe_status moe_pages_resize(int32_t* refs, int n_pages, int32_t* page_table, int
   b.len = own_len; b.new_len = new_len;
   const RowSet sets[] = {{refs, 1, 4ll * n_pages, 0}, {page_table, 1, 4ll * B * table_width, 0},
                          {own_len, 1, 4ll * B, 0}, {new_len, 1, 4ll * B, 0}};
-  return run_book(pages_resize_kernel, b, pools, n_pools, sets, 4, ws, ws_bytes, stream);
+  return run_book<false>(b, pools, n_pools, sets, 4, ws, ws_bytes, stream);
 }
 
 moe_status moe_pages_fork(int32_t* refs, int n_pages, int32_t* page_table, int B, int table_width, int page_size,
@@ -566,7 +604,7 @@ moe_status moe_pages_fork(int32_t* refs, int n_pages, int32_t* page_table, int B
   b.len = own_len; b.src = src; b.dst = dst; b.n = n;
   const RowSet sets[] = {{refs, 1, 4ll * n_pages, 0}, {page_table, 1, 4ll * B * table_width, 0},
                          {own_len, 1, 4ll * B, 0}, {src, 1, 4ll * n, 0}, {dst, 1, 4ll * n, 0}};
-  return run_book(pages_fork_kernel, b, pools, n_pools, sets, 5, ws, ws_bytes, stream);
+  return run_book<true>(b, pools, n_pools, sets, 5, ws, ws_bytes, stream);
 }
 
 moe_status moe_pages_compact(const int32_t* page_table, int n_pages, int B, int table_width, int page_size,
@@ -594,7 +632,7 @@ moe_status moe_pages_compact(const int32_t* page_table, int n_pages, int B, int 
   p.table = page_table; p.base = base; p.keep = keep; p.new_len = new_len;
   p.status = static_cast<int32_t*>(ws);
   const dim3 grid(B, n_pools > 0 ? n_pools : 1);
-  return launch(pages_compact_kernel, p, grid, kCompactThreads, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch(pages_compact_kernel, grid, kCompactThreads, 1, stream, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

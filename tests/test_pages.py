@@ -298,6 +298,23 @@ def test_random_walk(B, width, page, n_pages, seed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page,pools", [(8, POOLS), (1024, [("rows", 512), ("kv4", 5, 128)]), (256, [("rows", 2048), ("kv4", 1, 64)])])
+def test_shared_pages_that_are_written_on(page, pools):
+    """Every request of a resize takes a copy of a page that others hold too: of small
+    pools, and of pools so large that copies are a launch of their own."""
+    s = State(Model(9, 2, page, 30), pools)
+    s.resize([page // 2 + 1, page - 1, 1] + [0] * 6)
+    s.fork([(0, 3), (1, 4), (2, 5), (0, 6), (0, 7), (1, 8)])
+    m = s.m
+    for b in range(9):  # shared once more, as a prefix that another table holds would be
+        m.refs[m.table[b][0]] += 1
+    s.refs.copy_(_i32(m.refs))
+    s.resize([min(2 * page, n + 3) for n in m.len])
+    assert len({t[0] for t in m.table}) == 9
+    s.resize([n - 1 for n in m.len])
+
+
+@pytest.mark.gpu
 def test_many_pages_and_requests():
     """More pages and requests than a CTA has threads, in one call."""
     B, width, page, n_pages = 1500, 3, 8, 9000
