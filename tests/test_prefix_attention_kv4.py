@@ -438,3 +438,22 @@ def test_long_prompts(D, causal):
             assert off.max() <= torch.finfo(BF).eps
             assert (lse[t0:t0 + n, h].double() - torch.logsumexp(z, -1)).abs().max() <= 1e-4
     assert b.ws.device_status() == (ops.MOE_OK, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,page", [(1, 16), (4, 64)])
+def test_same_bits_from_cold_memory(n, page):
+    """Copies that land late and in any order: long requests on scattered pages, call behind
+    call, with what lies in L2 replaced between some of them."""
+    batch = Batch4(8, 2, 128, BF, page, 0, [(n, 9000 + 700 * b) for b in range(12)], seed=n)
+    batch.check(True)
+    want = [t.clone() for t in batch.run(True)]
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for turn in range(60):
+        if turn % 3 == 0:
+            other.fill_(turn)
+        for got, w in zip(batch.run(True), want):
+            differ += (got != w).sum()
+    assert differ.item() == 0
+    assert batch.ws.device_status() == (ops.MOE_OK, 0)
