@@ -276,14 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = tiles.at; t < tiles.end && ok; t += tiles.step)
       for (int kb = tiles.kb0; kb < tiles.kb1; ++kb, odd ^= 1, r.next(p.stages)) {
         if (odd != turn >> 1) continue;
-        ok = warp_wait(c, &c.full[r.stage], r.phase, p.status, kInfoFull);
-        if (!ok) break;
-        const uint8_t* st = mem + r.stage * stage_space + x_bytes;
-        uint4 w = *reinterpret_cast<const uint4*>(st + (half * 2 * kRows + row) * 16);
+        // (first the products of the block before the last: then every copy up to that one has
+        // landed, and the stage's parity can mean only this block's, with three stages too)
         ok = warp_wait(c, &c.a_empty[turn], phase, p.status, kInfoAccEmpty);
         if (!ok) break;
         phase ^= 1u;
         tc_fence_after();
+        ok = warp_wait(c, &c.full[r.stage], r.phase, p.status, kInfoFull);
+        if (!ok) break;
+        const uint8_t* st = mem + r.stage * stage_space + x_bytes;
+        uint4 w = *reinterpret_cast<const uint4*>(st + (half * 2 * kRows + row) * 16);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};

@@ -301,3 +301,20 @@ def test_both_kernels_agree_on_integers():
     for a in range(0, 40, 10):
         part = ops.linear_q4(c.x[a:a + 10], c.w, c.ws)
         assert torch.equal(part, whole[a:a + 10])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(128, 8192, 4096), (72, 8192, 4096), (256, 4096, 10240)])
+def test_same_bits_from_cold_memory(M, K, N):
+    """Copies that land late and in any order, with rings of three stages and more: call behind
+    call, with what lies in L2 replaced between some of them."""
+    c = Case(M, K, N, 128, seed=M)
+    want = c.check().clone()
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for turn in range(60):
+        if turn % 3 == 0:
+            other.fill_(turn)
+        differ += (c.run() != want).sum()
+    assert differ.item() == 0
+    assert c.ws.device_status() == (ops.MOE_OK, 0)
