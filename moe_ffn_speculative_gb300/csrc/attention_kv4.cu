@@ -40,13 +40,13 @@
 // it is fetched (a tile took 1.7 times as long with the four groups of the expansion
 // unrolled).
 //
-// Measured: 8 blocks of 9 tokens over 4096 shared keys and up to 900 own ones 30.5 us (32.4
-// when it signalled its joining launch early); 13 blocks of 8 over 30011, D = 64, 79 us; 64
-// blocks of 9 over 16384 and up to 2000, 347 us, 2250 clocks a tile of 64 rows.  Of those, without the expansion of keys 316, without that
-// of values 307, without the second product 331, without exponentials 343; without any of
-// them 255: what is left is one role waiting for another, at some ten clocks an instruction.
-// A second warpgroup for the values' expansion (338), one for the keys' (360) or issue by
-// whole warps were no faster throughout.
+// Measured: 8 blocks of 9 tokens over 4096 shared keys and up to 900 own ones 29.4 us (2 more
+// when it signalled its joining launch early); 13 blocks of 8 over 30011, D = 64, 77 us; 64
+// blocks of 9 over 16384 and up to 2000, 347 us, 2250 clocks a tile of 64 rows.  Of those,
+// without the expansion of keys 316, without that of values 307, without the second product
+// 331, without exponentials 343; without any of them 255: what is left is one role waiting
+// for another, at some ten clocks an instruction.  A second warpgroup for the values'
+// expansion (338), one for the keys' (360) or issue by whole warps were no faster throughout.
 //
 // Keys past a length are never read as numbers: their codes are replaced by zeros, and
 // their scores before the maximum.
@@ -719,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attention_kv4_kernel(const
     tmem_relinquish();
   }
   griddep_wait();               // what the previous kernel on the stream wrote is visible
-  const int plen = find_share<kThreads>(p, c.start);
+  int plen = 0;
+  if (p.B > kWarpRequests) plen = find_share<kThreads>(p, c.start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -741,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attention_kv4_kernel(const
       __syncwarp();
       drain_mma(p, c, 1);
     } else {
+      if (p.B <= kWarpRequests) plen = find_share_by_warp(p, c.start);
       hand_list(p, c, plen);
       __syncwarp();
     }

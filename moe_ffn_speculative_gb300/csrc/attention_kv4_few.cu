@@ -540,9 +540,11 @@ __global__ void __launch_bounds__(threads(kBlocks), 1) kv4_few_kernel(const __gr
     fence_barrier_init();
   }
   griddep_wait();               // what the previous kernel on the stream wrote is visible
-  const int plen = find_share<Geo::kThreads>(p, c.start);
+  int plen = 0;
+  if (p.B > kWarpRequests) plen = find_share<Geo::kThreads>(p, c.start);
   __syncthreads();
   if (warp == Geo::kWarps) {
+    if (p.B <= kWarpRequests) plen = find_share_by_warp(p, c.start);
     produce<D, kBlocks>(p, c, plen, mem + Geo::kRingAt);
     return;
   }
@@ -596,8 +598,8 @@ cudaError_t launch(const Kv4Attn& p, int rows, cudaStream_t s) {
 }  // namespace
 
 // A tile of 128 keys costs this kernel 0.55 of what the other needs for up to 64 rows where
-// it has up to 8 (640000 own keys of 16 single tokens: 139 us, the other 257), 0.81 where it
-// has up to 16 (4 tokens each: 209 and 257; at 80000 keys 50 and 48).  So it takes a call
+// it has up to 8 (640000 own keys of 16 single tokens: 146 us, the other 257), 0.82 where it
+// has up to 16 (4 tokens each: 212 and 257; at 80000 keys 50 and 48).  So it takes a call
 // whose blocks have few rows unless a prefix shared by many of them outweighs their own keys,
 // as far as the tables' sizes tell (8 blocks of 12 rows over 4096 shared keys and up to 900
 // own ones: 32.8 us here, 27.8 there).

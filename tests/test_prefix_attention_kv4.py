@@ -148,7 +148,7 @@ def test_against_definition(name):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B", [1, 500, 1100])
+@pytest.mark.parametrize("B", [1, 31, 32, 33, 500, 1100])
 def test_many_blocks(B):
     """More requests than a block of threads looks at in one step."""
     Batch4(2, 1, 64, BF, 8, 40, [(i % 2, (5 * i) % 40) for i in range(B)], seed=B).check(True)
