@@ -392,8 +392,10 @@ __global__ void __launch_bounds__(kCompactThreads) pages_compact_kernel(const __
   __syncthreads();
   for (int j = tid; j < listed; j += kCompactThreads) {
     const int o = keep[j], before = j > 0 ? keep[j - 1] : -1;
-    // offsets grow and lie in the table, as do the rows that they go to
-    bool bad = o <= before || o >= cap - base;
+    // offsets grow and lie in the table, as do the rows that they go to: an entry behind one
+    // out of order is looked at too, and with o >= j (true of every list that grows) its
+    // place base + j <= base + o lies in the table as well
+    bool bad = o <= before || o < j || o >= cap - base;
     if (!bad) {
       const int from = row[(base + o) >> p.page_log2], to = row[(base + j) >> p.page_log2];
       bad = static_cast<uint32_t>(from) >= static_cast<uint32_t>(p.n_pages) ||
