@@ -601,12 +601,14 @@ struct Softmax {
     float l[kMine];
 #pragma unroll
     for (int r = 0; r < kMine; ++r) l[r] = 0.f;
+    // (the rows may have been another group's in the segment before, which it is done with once
+    // all warps have brought their queries)
+    bool ok = warp_wait(c, &c.q_full, seg & 1, p.status, kInfoAttnQuery);
     if (key < kMine) {
       c.m[row0 + key] = -INFINITY;
       c.neg[row0 + key] = 0.f;
     }
     softmax_sync(group);
-    bool ok = warp_wait(c, &c.q_full, seg & 1, p.status, kInfoAttnQuery);
     int j = s.j0;
     for (; j + 1 < s.j1; j += 2, i += 2)
       if (!step<kMine, 2>(s, seg, i, j, l, ok)) return false;
