@@ -622,7 +622,9 @@ struct Softmax {
     tc_fence_after();
     if (key < kMine && row0 + key < rows) {
       const int r = row0 + key;
-      p.ml[s.part_row + r] = make_float2(c.m[r], (c.top[0][r] + c.top[1][r]) + (c.top[2][r] + c.top[3][r]));
+      const float sum = (c.top[0][r] + c.top[1][r]) + (c.top[2][r] + c.top[3][r]);
+      // (a row whose scores were all NaN has no reference: without one its part would count as empty)
+      p.ml[s.part_row + r] = make_float2(isnan(sum) ? NAN : c.m[r], sum);
     }
     // channels are lanes: a row is written 128 bytes a warp
     const uint32_t o = tmem + Geo::kOutCol + qb * kRows + lanes;
