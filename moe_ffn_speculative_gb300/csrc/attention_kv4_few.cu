@@ -522,7 +522,8 @@ __device__ __forceinline__ void finish(const Kv4Attn& p, const Control& c, const
     float* dst = p.o + (s.part_row + row0 + row) * D + lane;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) dst[32 * i] = acc[i];
-    if (lane == 0) p.ml[s.part_row + row0 + row] = make_float2(top, sum);
+    // (a row whose scores were all NaN has no reference: without one its part would count as empty)
+    if (lane == 0) p.ml[s.part_row + row0 + row] = make_float2(isnan(sum) ? NAN : top, sum);
   }
 }
 

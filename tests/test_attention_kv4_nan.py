@@ -69,3 +69,15 @@ def test_many_rows(n, own, P, D, dtype, causal):
     a tile and more."""
     for f in (_queries, _last_key):
         f(Batch4(8, 2, D, dtype, 16, P, [(n, own), (n, own + 3)], seed=n), causal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, HF)])
+@pytest.mark.parametrize("Hq,Hkv,n,own,P", [(64, 8, 1, 5, 0), (64, 8, 1, 1, 0), (64, 8, 1, 300, 0), (64, 8, 2, 5, 0),
+                                            (32, 8, 1, 5, 0), (32, 8, 4, 3, 0), (32, 8, 2, 700, 3), (16, 1, 1, 5, 3)])
+def test_few_rows(Hq, Hkv, n, own, P, D, dtype, causal):
+    """Blocks of 4, 8 and 16 rows a key head, all of them NaN and some, keys for one warp and
+    for several."""
+    for f in (_queries, _last_key):
+        f(Batch4(Hq, Hkv, D, dtype, 16, P, [(n, own), (n, own + 3)], seed=n), causal)
