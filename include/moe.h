@@ -739,7 +739,8 @@ MOE_API moe_status moe_pages_fork(int32_t* refs, int n_pages, int32_t* page_tabl
  * drafts, say) begins at token base[b], the row of token base[b] + keep[b][j] goes to token base[b] +
  * j, for j up to the first negative entry; new_len[b] = base[b] + their number (what
  * moe_pages_resize takes next).  A page that another request holds too must not be
- * among those moved into (moe_pages_resize to the block's end sees to it).
+ * among those moved into: moe_pages_resize to the block's end sees to it, and of a request
+ * that it refused (its own_len is less than the block's end) nothing may be kept.
  *   keep       [B, n] int32, n <= MOE_MAX_BLOCK, growing; an entry that does not grow, or
  *              whose row or place is outside the table or the pool, is recorded
  *              (MOE_INFO_KEEP) and ends the list

@@ -188,8 +188,11 @@ class PagedRequests:
 
     def keep(self, base: torch.Tensor, kept: torch.Tensor) -> None:
         """Of a block's tokens those at offsets kept [requests, n] stay (growing, the
-        first negative one ends a row), moved up behind the first `base` ones."""
-        self.resize(ops.pages_compact(self.table, base, kept, self.page, self.ws, self.caches))
+        first negative one ends a row), moved up behind the first `base` ones.  A request
+        that `block` found no pages for has no block to keep of: it stays as it was."""
+        # (its last page may still be another request's too, which a move would write into)
+        granted = torch.where(base[:, None] + kept < self.own_len[:, None], kept, -1)
+        self.resize(ops.pages_compact(self.table, base, granted, self.page, self.ws, self.caches))
 
 
 def shared_prefix_batch(requests: int, block: int, prefix: int, own: int, page: int, device="cuda") -> Batch:
