@@ -75,6 +75,12 @@ __device__ __forceinline__ void record_pool(int32_t* status) {
   if (atomicCAS(status, 0, kStatusPool) == 0) atomicExch(status + 1, kInfoPool);
 }
 
+// What requests need can pass 32 bits in all (65536 of them, 2^25 pages each); how many there
+// are cannot (n_pages < 2^28).  Sums stop at a number above that: a request at or past it is
+// refused, whatever it would be.
+constexpr int kManyPages = 1 << 29;
+__device__ __forceinline__ int add_pages(int a, int b) { return min(a + b, kManyPages); }
+
 // Exclusive prefix sum over the CTA; `total` gets the sum of all.
 __device__ int block_scan(int v, int& total) {
   __shared__ int sums[kBookThreads / 32];
@@ -83,16 +89,17 @@ __device__ int block_scan(int v, int& total) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
+    if (lane >= o) inc = add_pages(inc, u);
   }
   if (lane == 31) sums[warp] = inc;
+  const int left = __shfl_up_sync(0xffffffffu, inc, 1);
   __syncthreads();
   if (warp == 0) {
     int s = sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
+      if (lane >= o) s = add_pages(s, u);
     }
     sums[lane] = s;
   }
@@ -100,7 +107,7 @@ __device__ int block_scan(int v, int& total) {
   const int before = warp > 0 ? sums[warp - 1] : 0;
   total = sums[kBookThreads / 32 - 1];
   __syncthreads();
-  return before + inc - v;
+  return add_pages(before, lane > 0 ? left : 0);
 }
 
 // The lowest `need` free pages in order, to p.list; -> how many there are of them.
@@ -192,7 +199,7 @@ __device__ void resize_book(const BookParams& p) {
     int total;
     const int first = need + block_scan(mine, total);
     if (b < p.B) p.state[b] = make_int4(first, what, old, now);
-    need += total;
+    need = add_pages(need, total);
   }
   __syncthreads();
   const int found = need > 0 ? find_free(p, need) : 0;
