@@ -784,9 +784,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const __grid_c
   const int t = static_cast<int>(unit / p.Hq), hq = static_cast<int>(unit % p.Hq), h = hq / p.G, g = hq % p.G;
   griddep_wait();
   const Plan plan = *p.plan;
-  // (a token outside every request reads what an earlier call left: checked)
-  RequestPlan rp = {0, 0, 0, 0};
-  if (p.B > 0) rp = p.requests[t];
+  // (the search for the shares has written every token's of this call: zeros for one of no
+  // request, which owns nothing; what an earlier call left is never read)
+  const RequestPlan rp = p.requests[t];
   const bool owned = t >= rp.a && t < rp.a + rp.n;
   const Request rq = {rp.a, rp.n, rp.len, true};
   float m = -INFINITY, l = 0.f, acc[kEach];
