@@ -670,7 +670,8 @@ MOE_API moe_status moe_kv4_read(const void* cache, int n_pages, int page_size, i
  * The keys and values enter both products exactly, in f16; a bf16 query row is scaled
  * by a power of two first, and its elements are held to 2^-40 of its largest (exact
  * down to 2^-31 of it); the probabilities enter in f16, each to within 2^-32 of the
- * row's largest. */
+ * row's largest.  A row whose query holds a NaN, or that sees a NaN key, is NaN in out and
+ * lse; one that sees no key is 0 and -infinity. */
 MOE_API size_t moe_prefix_attention_kv4_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
 MOE_API moe_status moe_prefix_attention_kv4(const void* q, long long q_stride, int T, int B, const int32_t* q_start,
                                             int Hq, int Hkv, int D, int dtype, const void* cache, int n_pages,

@@ -40,8 +40,8 @@
 // it is fetched (a tile took 1.7 times as long with the four groups of the expansion
 // unrolled).
 //
-// Measured: 8 blocks of 9 tokens over 4096 shared keys and up to 900 own ones 29.4 us (2 more
-// when it signalled its joining launch early); 13 blocks of 8 over 30011, D = 64, 77 us; 64
+// Measured: 8 blocks of 9 tokens over 4096 shared keys and up to 900 own ones 29.0 us (2 more
+// when it signalled its joining launch early); 13 blocks of 8 over 30011, D = 64, 78 us; 64
 // blocks of 9 over 16384 and up to 2000, 347 us, 2250 clocks a tile of 64 rows.  Of those,
 // without the expansion of keys 316, without that of values 307, without the second product
 // 331, without exponentials 343; without any of them 255: what is left is one role waiting

@@ -342,9 +342,13 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 // The bookkeeping alone (a CTA), or with its copies (a cluster, which does them once its
 // first CTA has listed them: one launch in place of two, but the copies on 8 SMs).  A
 // resize copies only what goes on being written while another request shares it, mostly
-// nothing: 8 requests in 5 pools take 3.9 us like this and 5.4 with two launches; if all of
-// them copy a page (2.8 MB), 13.3 and 7.1.  So it is taken where no more than kFewBytes can
-// have to be copied; a fork, which always copies, has two launches.
+// nothing: 8 requests in 5 pools take 4.1 us like this and 5.4 with two launches; if all of
+// them copy a page (2.8 MB), 13.6 and 7.2.  So it is taken where no more than kFewBytes can
+// have to be copied; a fork, which always copies, has two launches.  By the bytes that a call
+// may have to copy (one launch with none of them copied and with all; two launches): 0.7 MB
+// 3.8 and 7.4 to 8.7 us, 5.4 and 6.6; 5.6 MB 3.8 and 21, 5.5 and 7.3; 11 MB 4.1 and 34, 5.4 and
+// 8.6; 45 MB 4.6 and 120, 5.9 and 17.  At the line a call that copies everything loses what
+// some six that copy nothing win.
 template <bool kFork, bool kCopies>
 __global__ void __launch_bounds__(kBookThreads) pages_book_kernel(const __grid_constant__ BookParams b, const __grid_constant__ CopyParams c) {
   griddep_wait();

@@ -187,9 +187,10 @@ class PagedRequests:
                      page_table=self.table, prefix_pages=self.prefix_pages, prefix_len=prefix_len), base
 
     def keep(self, base: torch.Tensor, kept: torch.Tensor) -> None:
-        """Of a block's tokens those at offsets kept [requests, n] stay (growing, the
-        first negative one ends a row), moved up behind the first `base` ones.  A request
-        that `block` found no pages for has no block to keep of: it stays as it was."""
+        """Of a block's tokens those at offsets kept [requests, n] stay (growing; the first
+        negative one, or one past the block, ends a row), moved up behind the first `base`
+        ones.  A request that `block` found no pages for has no block to keep of: it stays as
+        it was."""
         # (its last page may still be another request's too, which a move would write into)
         granted = torch.where(base[:, None] + kept < self.own_len[:, None], kept, -1)
         self.resize(ops.pages_compact(self.table, base, granted, self.page, self.ws, self.caches))
